@@ -80,6 +80,8 @@ typedef enum {
 #define ZO_FLAG_NONFINITE 0x1u /* a loss was not finite; that step was skipped */
 #define ZO_FLAG_TIMEOUT 0x2u   /* a tensor-core kernel's pipeline wait expired (about 2 s);
                                   its output is invalid */
+#define ZO_FLAG_OFFSETS 0x4u   /* an array of sequence offsets decreased or left its buffer;
+                                  those sequences' outputs were not written */
 
 /* Largest n_pert accepted by zo_step / zo_update (the update keeps a 1 KB table per
  * group of 8 probes in shared memory: 128 KB at this limit). */
@@ -126,8 +128,8 @@ const void *zo_live_params(const zo_ctx *ctx);
 
 /* Synchronise the context's stream and return the sticky device flags (ZO_FLAG_*)
  * raised since the last call, clearing them; *flags may be NULL.  Returns
- * ZO_ERR_TIMEOUT if ZO_FLAG_TIMEOUT was raised, else ZO_ERR_NONFINITE if
- * ZO_FLAG_NONFINITE was raised, else ZO_OK. */
+ * ZO_ERR_TIMEOUT if ZO_FLAG_TIMEOUT was raised, else ZO_ERR_INVALID if ZO_FLAG_OFFSETS was,
+ * else ZO_ERR_NONFINITE if ZO_FLAG_NONFINITE was raised, else ZO_OK. */
 zo_status zo_sync(zo_ctx *ctx, uint32_t *flags);
 
 /* Read (synchronising) or set (enqueued) the device-resident step counter, which keys
@@ -605,6 +607,124 @@ zo_status zo_rmsnorm(zo_ctx *ctx, const float *x, const void *w, void *out, int3
  * d <= 8192, d % 8 == 0, pointers 16-byte aligned. */
 zo_status zo_layernorm(zo_ctx *ctx, const float *x, const void *gamma, const void *beta,
                        void *out, int32_t rows, int32_t d);
+
+/* ------------------------------------------------------------------ packed prompts */
+
+/* Scoring prompts of different lengths without padding: the tokens of all sequences lie one
+ * after another in the rows of a batch, sequence i in rows cu_seqlens[i] .. cu_seqlens[i+1]-1.
+ * A forward pass over such a batch is the projections and norms above (which treat every row
+ * alike), zo_rope with each token's position, zo_attention_packed, and, for a loss on given
+ * tokens, zo_head_logprobs (or zo_logprobs where the logits are wanted anyway).  Forward only,
+ * like every loss here: the method takes no gradients ("Probe-Space Preconditioning for Fast
+ * and Stable Zero-Order Training", abstract).  These calls read nothing of the context's
+ * parameters; they use its device (made current for the call), stream and flags, allocate
+ * nothing and hold no state, so that they may be captured into graphs. */
+
+/* Scaling of the rotary angles for sequences longer than those trained on. */
+#define ZO_ROPE_PLAIN 0   /* f_i = theta^(-2 i / rot_dim) */
+#define ZO_ROPE_LINEAR 1  /* f_i / factor (interpolated positions) */
+#define ZO_ROPE_BANDS 2   /* by bands of wavelength: with n_i = orig_len f_i / (2 pi) turns over
+                           * the trained length and g_i = (n_i - band_low) / (band_high -
+                           * band_low) clamped to [0, 1]: g_i f_i + (1 - g_i) f_i / factor */
+
+typedef struct {
+  float theta;          /* base, > 0 */
+  int32_t rot_dim;      /* leading features of a head that are rotated: even, 2 .. head_dim */
+  int32_t interleaved;  /* 0: feature i pairs with i + rot_dim/2;  1: 2 i pairs with 2 i + 1 */
+  int32_t scaling;      /* ZO_ROPE_* */
+  float factor;         /* ZO_ROPE_LINEAR, ZO_ROPE_BANDS: > 0 */
+  float orig_len;       /* ZO_ROPE_BANDS: > 0 */
+  float band_low, band_high; /* ZO_ROPE_BANDS: turns, low < high */
+  float magnitude;      /* multiplies the rotated features (1: a pure rotation); finite */
+} zo_rope_cfg;
+
+/* Largest head dimension of zo_rope. */
+#define ZO_ROPE_MAX_HEAD_DIM 256
+
+/* The rot_dim / 2 angular frequencies f_i of `cfg` in radians per position (host doubles), as
+ * zo_rope uses them.  Host only.  Errors: ZO_ERR_INVALID (null, a field outside its range). */
+zo_status zo_rope_frequencies(const zo_rope_cfg *cfg, double *radians);
+
+/* Rotary positions: out = x with the pairs (a, b) of every head's first rot_dim features
+ * replaced by magnitude * (a cos t - b sin t, b cos t + a sin t), t = positions[row] * f_i;
+ * the features behind rot_dim are copied.
+ *   x, out     device, `dtype` (ZO_F32 or ZO_BF16), rows of ldx and ldo elements, n_heads
+ *              heads of head_dim features from the start of each row (to rotate the query and
+ *              key heads of a fused projection, pass its rows and n_heads + n_kv_heads).
+ *              out == x (with ldo == ldx) rotates in place; otherwise the two must not overlap.
+ *   positions  device, int32 [rows] (any value), or NULL: row r has position r.
+ * Angles are formed and reduced in fp64 (within 2^-25 of a turn up to position 2^28, 2^-23 at the
+ * ends of int32); the rotation is fp32 arithmetic with one rounding to `dtype`.  Best when pointers, row strides and head_dim are
+ * multiples of 16 bytes.  1 <= rows < 2^31, 1 <= n_heads <= 65535, rot_dim <= head_dim <=
+ * ZO_ROPE_MAX_HEAD_DIM.  Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
+zo_status zo_rope(zo_ctx *ctx, const void *x, void *out, int dtype, const int32_t *positions,
+                  const zo_rope_cfg *cfg, int64_t rows, int64_t ldx, int64_t ldo, int32_t n_heads,
+                  int32_t head_dim);
+
+/* Causal grouped-query attention within each of n_seqs packed sequences: for query row i of
+ * a sequence, out_i = sum_j softmax_j(scale * q_i . k_j) v_j over the sequence's rows j <= i.
+ *   q, k, v     device bf16, total_tokens rows of ldq, ldk, ldv elements; query head h at
+ *               column h head_dim, key/value head h / (n_heads / n_kv_heads) likewise.  They
+ *               may be column ranges of one fused projection.
+ *   out         device bf16, total_tokens rows of ldo elements, head h at h head_dim; must not
+ *               overlap q, k or v.
+ *   cu_seqlens  device int32 [n_seqs + 1], not decreasing, within [0, total_tokens].  A sequence
+ *               may be empty.  Rows of out outside every sequence are not written.
+ *   scale       finite and > 0 (1/sqrt(head_dim) for the decoders here).
+ * fp32 scores and sums, probabilities rounded to bf16 for the second product, one bf16 rounding
+ * of the output.  A row depends on its sequence's rows up to itself only, whatever the other
+ * rows hold (infinities and NaN too).  The offsets are read on the device: a decreasing or
+ * out-of-range pair raises ZO_FLAG_OFFSETS (seen by zo_sync) and its sequence is skipped.
+ * n_heads % n_kv_heads == 0, head_dim 64 or 128, pointers 16-byte aligned, row strides multiples
+ * of 8 elements, 1 <= total_tokens < 2^31, 1 <= n_seqs.  Bounded waits as zo_gemm_bf16.
+ * Errors: ZO_ERR_INVALID, ZO_ERR_UNSUPPORTED (head_dim), ZO_ERR_CUDA. */
+zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void *k, const void *v, void *out,
+                              const int32_t *cu_seqlens, int32_t n_seqs, int64_t total_tokens,
+                              int64_t ldq, int64_t ldk, int64_t ldv, int64_t ldo, int32_t n_heads,
+                              int32_t n_kv_heads, int32_t head_dim, float scale);
+
+/* Most alternatives that zo_logprobs returns per row. */
+#define ZO_MAX_TOP 32
+
+/* Log probabilities from logits, row by row: with lse = log sum_j exp(x_j),
+ *   logprob[r] = x_target - lse,  entropy[r] = lse - sum_j p_j x_j  (natural logarithms),
+ *   top_ids[r][0..top-1] the indices of the top largest logits, largest first, equal values in
+ *   the order of their index, and top_logprobs[r][.] = x_id - lse.
+ *   logits   device, `dtype` (ZO_F32 or ZO_BF16), rows of ld elements, vocab of them used.
+ *   targets  device int32 [rows], or NULL with logprob NULL.  -1 scores nothing: logprob 0.
+ *            Any other value outside [0, vocab) gives NaN.
+ *   logprob, entropy  device fp32 [rows], either may be NULL.
+ *   top_ids (int32), top_logprobs (fp32)  device [rows][top]; either may be NULL, top = 0: none.
+ * A logit of -inf rules its token out (probability 0).  A row without any other logit, or with
+ * a NaN or +inf, has no distribution: its outputs are NaN (NaN logits sort before all others).
+ * Sums in fp32 over at most a few thousand terms each, joined in a fixed order, final
+ * logarithms in fp64: results do not vary from run to run.  1 <= vocab <= ld < 2^31,
+ * 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP, vocab).  Any alignment of the element type.
+ * Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
+zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int64_t rows, int64_t vocab,
+                      int64_t ld, const int32_t *targets, float *logprob, float *entropy, int32_t top,
+                      int32_t *top_ids, float *top_logprobs);
+
+/* Bytes of device workspace that zo_head_logprobs needs for these sizes (host only).
+ * Errors: ZO_ERR_INVALID (null, sizes outside zo_head_logprobs' limits). */
+zo_status zo_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t *bytes);
+
+/* logprob and entropy of zo_logprobs for the logits x[r][j] = hidden[r] . W[j], which are never
+ * in memory: fp32 products of bf16 operands on the tensor cores, their softmax statistics kept
+ * beside the accumulator, partial statistics joined by a second kernel in a fixed order.
+ *   hidden     device bf16, rows of ldh elements, width of them used.
+ *   W          device bf16, vocab rows of ldw elements (the head; for a perturbed one, the
+ *              window that zo_perturb_range wrote).
+ *   targets, logprob, entropy  as zo_logprobs (at least one output).
+ *   workspace  device, 16-byte aligned, zo_head_logprobs_workspace bytes; holds nothing between
+ *              calls.  Calls that may run at the same time need one each.
+ * Logits within +-1e8; a row with a NaN or +inf among its logits has NaN outputs, one with a -inf
+ * a NaN entropy.  width, ldh and ldw multiples of 8, hidden and W 16-byte aligned, rows, vocab,
+ * width, ldh, ldw >= 1 and < 2^31.  Bounded waits as zo_gemm_bf16.  Errors: ZO_ERR_INVALID (also a
+ * workspace that is too small), ZO_ERR_CUDA. */
+zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64_t rows, int64_t vocab,
+                           int64_t width, int64_t ldh, int64_t ldw, const int32_t *targets,
+                           float *logprob, float *entropy, void *workspace, int64_t workspace_bytes);
 
 #ifdef __cplusplus
 }

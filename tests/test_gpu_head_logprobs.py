@@ -1,0 +1,210 @@
+"""zo_head_logprobs against the product and log-softmax in 64 bits.
+
+Tolerances: a logit is an fp32 sum of `width` exact products, off by at most
+e_x = width 2^-23 max_j sum_i |h_i w_ji| whatever the order (2^-23: truncation); it moves lse and
+the given logit by e_x each.  The statistics add E = (vocab / 16 + 24) 2^-24 + 2^-21 at most (a
+thread sums every fourth or rarer column of its range; the bound takes one in 16 of all), as in
+the tests of zo_logprobs:
+    |logprob - ref| <= 2 e_x + E + 2^-25 (max - x_t) + 2^-24 |ref|,
+    |H - ref| <= (E + 2 e_x) (1 + 2 sum_j p_j (max - x_j)) + 2^-24 |ref| + 2 e_x.
+"""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ctx(zo):
+    c = zo.zo_create(torch.zeros(64, dtype=torch.bfloat16, device="cuda"))
+    yield c
+    c.close()
+
+
+def make(rows, vocab, width, seed=0, scale=None, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + rows + vocab + width)
+    h = torch.randn(rows, width + pad, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(vocab, width + pad, generator=g, device="cuda") * (2.0 / math.sqrt(width) if scale is None else scale)
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    return h, w.to(torch.bfloat16), t
+
+
+def call(zo, ctx, h, w, t, width=None, guard=256):
+    rows, vocab = len(h), len(w)
+    width = h.shape[1] if width is None else width
+    n = zo.zo_head_logprobs_workspace(rows, vocab)
+    space = torch.full((n + guard,), 0xAB, dtype=torch.uint8, device="cuda")
+    lp, ent = torch.full((rows,), 9.0, device="cuda"), torch.full((rows,), 9.0, device="cuda")
+    zo.zo_head_logprobs(ctx, h, w, rows, vocab, width, h.stride(0), w.stride(0), t, lp, ent, space, n)
+    assert zo.zo_sync(ctx) == 0
+    assert torch.all(space[n:] == 0xAB)  # nothing behind the workspace
+    return lp, ent
+
+
+def check(h, w, t, got):
+    lp, ent = got
+    vocab, width = w.shape
+    E = (vocab / 16 + 24) * 2.0 ** -24 + 2.0 ** -21
+    for a in range(0, len(h), 512):
+        H, T = h[a: a + 512].double(), t[a: a + 512].long()
+        x = H @ w.double().T
+        e = width * 2.0 ** -23 * (H.abs() @ w.double().abs().T).amax(1)
+        ref = torch.log_softmax(x, 1)
+        p = ref.exp()
+        big = x.amax(1, keepdim=True)
+        spread = (p * (big - x)).sum(1)
+        want = torch.where(T >= 0, ref.gather(1, T.clamp(min=0)[:, None])[:, 0], torch.zeros_like(spread))
+        gap = big[:, 0] - x.gather(1, T.clamp(min=0)[:, None])[:, 0]
+        tol = 2 * e + E + 2.0 ** -25 * gap + 2.0 ** -24 * want.abs()
+        off = (lp[a: a + 512].double() - want).abs()
+        assert torch.all(off <= tol), (off / tol).max()
+        ref_h = -(p * ref).sum(1)
+        tol = (E + 2 * e) * (1 + 2 * spread) + 2.0 ** -24 * ref_h + 2 * e
+        off = (ent[a: a + 512].double() - ref_h).abs()
+        assert torch.all(off <= tol), (off / tol).max()
+
+
+SIZES = [(1, 1, 8), (1, 2, 8), (3, 31, 16), (5, 32, 64), (1, 33, 72), (7, 257, 128), (127, 1000, 64), (128, 4736, 64),
+         (129, 5000, 136), (16, 50272, 768), (1, 30001, 1024), (200, 9999, 512), (300, 500, 264), (1000, 3001, 64),
+         (2049, 1200, 128), (513, 40000, 192), (4096, 20011, 64)]
+
+
+@pytest.mark.parametrize("rows,vocab,width", SIZES)
+def test_head_logprobs_match(zo, ctx, rows, vocab, width):
+    h, w, t = make(rows, vocab, width)
+    check(h, w, t, call(zo, ctx, h, w, t))
+
+
+@pytest.mark.parametrize("scale", [1e-4, 1.0])
+def test_flat_and_peaked_distributions(zo, ctx, scale):
+    h, w, t = make(70, 7000, 256, scale=scale)
+    t[:35] = (h[:35].double() @ w.double().T).argmax(1).to(torch.int32)
+    check(h, w, t, call(zo, ctx, h, w, t))
+
+
+@pytest.mark.parametrize("rows,vocab", [(40, 3000), (700, 3000), (1200, 9000)])
+def test_strides(zo, ctx, rows, vocab):
+    """Padded rows full of NaN behind the width."""
+    h, w, t = make(rows, vocab, 200, pad=24)
+    h[:, 200:] = math.nan
+    w[:, 200:] = math.nan
+    check(h[:, :200], w[:, :200], t, call(zo, ctx, h, w, t, width=200))
+
+
+@pytest.mark.parametrize("rows", [3, 600])
+def test_each_target_position_is_found(zo, ctx, rows):
+    """Targets on every unit and tile edge, the first and the last."""
+    vocab = 4111
+    h, w, t = make(rows, vocab, 64)
+    edges = [0, 1, 31, 32, 63, 64, 127, 128, 255, 256, 257, 4095, 4096, 4110]
+    for a in range(0, len(edges), rows):
+        part = torch.tensor(edges[a: a + rows], dtype=torch.int32, device="cuda")
+        t[: len(part)] = part
+        check(h, w, t, call(zo, ctx, h, w, t))
+
+
+@pytest.mark.parametrize("rows", [6, 400])
+def test_targets_outside_and_not_scored(zo, ctx, rows):
+    h, w, t = make(rows, 500, 64)
+    t[:5] = torch.tensor([-1, 500, -2, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    lp, ent = call(zo, ctx, h, w, t)
+    assert lp[0] == 0 and torch.isnan(lp[1:5]).all() and torch.isfinite(ent).all()
+    check(h[5:], w, t[5:], (lp[5:], ent[5:]))
+
+
+@pytest.mark.parametrize("rows", [9, 500])
+def test_bad_rows_stay_their_own(zo, ctx, rows):
+    h, w, t = make(rows, 2000, 128)
+    want = call(zo, ctx, h, w, t)
+    h[2, 5] = math.nan
+    h[4] = math.inf
+    lp, ent = call(zo, ctx, h, w, t)
+    assert torch.isnan(lp[[2, 4]]).all() and torch.isnan(ent[[2, 4]]).all()
+    keep = [i for i in range(rows) if i not in (2, 4)]
+    assert torch.equal(lp[keep], want[0][keep]) and torch.equal(ent[keep], want[1][keep])
+
+
+@pytest.mark.parametrize("rows", [4, 900])
+def test_repeatable_and_one_output_only(zo, ctx, rows):
+    h, w, t = make(rows, 20000, 256)
+    lp, ent = call(zo, ctx, h, w, t)
+    again = call(zo, ctx, h, w, t)
+    assert torch.equal(lp, again[0]) and torch.equal(ent, again[1])
+    n = zo.zo_head_logprobs_workspace(rows, 20000)
+    space = torch.empty(n, dtype=torch.uint8, device="cuda")
+    a, b = torch.zeros_like(lp), torch.zeros_like(ent)
+    zo.zo_head_logprobs(ctx, h, w, rows, 20000, 256, 256, 256, t, a, None, space)
+    zo.zo_head_logprobs(ctx, h, w, rows, 20000, 256, 256, 256, None, None, b, space)
+    assert torch.equal(a, lp) and torch.equal(b, ent)
+
+
+def test_agrees_with_logits_in_memory(zo, ctx):
+    """The same rows through zo_gemm_bf16 (fp32 output) and zo_logprobs."""
+    h, w, t = make(256, 5000, 512)
+    x = torch.zeros(256, 5000, device="cuda")
+    zo.zo_gemm_bf16(ctx, h, w, None, x, 256, 5000, 512, 5000, zo.ZO_EPI_RESID_F32)
+    a, b = torch.zeros(256, device="cuda"), torch.zeros(256, device="cuda")
+    zo.zo_logprobs(ctx, x, 256, 5000, 5000, t, a, b)
+    lp, ent = call(zo, ctx, h, w, t)
+    e = 512 * 2.0 ** -23 * (h.double().abs() @ w.double().abs().T).amax(1)
+    assert torch.all((lp.double() - a).abs() <= 4 * e + 1e-4) and torch.all((ent.double() - b).abs() <= 20 * e + 1e-4)
+
+
+@pytest.mark.parametrize("rows", [20, 512])
+def test_replayed(zo, rows):
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        c = zo.zo_create(torch.zeros(64, device="cuda"), stream=s)
+        h, w, t = make(rows, 4000, 128)
+        lp, ent = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+        space = torch.empty(zo.zo_head_logprobs_workspace(rows, 4000), dtype=torch.uint8, device="cuda")
+        # once before the capture, as any kernel's first launch sets it up
+        zo.zo_head_logprobs(c, h, w, rows, 4000, 128, 128, 128, t, lp, ent, space)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        zo.zo_head_logprobs(c, h, w, rows, 4000, 128, 128, 128, t, lp, ent, space)
+    for seed in (5, 6):
+        with torch.cuda.stream(s):
+            h.copy_(make(rows, 4000, 128, seed=seed)[0])
+            g.replay()
+        s.synchronize()
+        check(h, w, t, (lp, ent))
+    del g
+    c.close()
+
+
+def test_head_refusals(zo, ctx):
+    h, w, t = make(4, 100, 64)
+    lp, ent = torch.full((4,), 9.0, device="cuda"), torch.full((4,), 9.0, device="cuda")
+    n = zo.zo_head_logprobs_workspace(4, 100)
+    space = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    base = dict(h=h, w=w, rows=4, vocab=100, width=64, ldh=64, ldw=64, t=t, lp=lp, ent=ent, space=space, n=n)
+
+    def refused(**k):
+        a = dict(base, **k)
+        with pytest.raises(zo.ZoError) as e:
+            zo.zo_head_logprobs(ctx, a["h"], a["w"], a["rows"], a["vocab"], a["width"], a["ldh"], a["ldw"], a["t"],
+                                a["lp"], a["ent"], a["space"], a["n"])
+        assert e.value.status == zo.ZO_ERR_INVALID
+
+    for name in ("h", "w", "space"):
+        refused(**{name: 0})
+    for name in ("h", "w", "space"):
+        refused(**{name: a.data_ptr() + 8 if (a := base[name]) is not None else 0})
+    for name in ("rows", "vocab", "width"):
+        refused(**{name: 0})
+    refused(rows=1 << 31)
+    refused(vocab=1 << 31)
+    refused(width=60)
+    refused(width=72)
+    refused(ldh=60)
+    refused(ldw=68)
+    refused(t=None)
+    refused(lp=None, ent=None)
+    refused(n=n - 1)
+    refused(lp=lp.data_ptr() + 2)
+    torch.cuda.synchronize()
+    assert torch.all(lp == 9.0)

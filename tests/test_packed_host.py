@@ -1,0 +1,131 @@
+"""Host side of the packed-prompt operators, without a GPU: rotary frequencies and their
+refusals, the workspace size, null contexts, and the block-to-work arithmetic of the kernels
+restated in Python."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+PLAIN = dict(theta=1.0e4, rot_dim=64)
+BANDS = dict(theta=1.0e6, rot_dim=128, scaling="bands", factor=4.0, orig_len=4096.0, band_low=1.0,
+             band_high=32.0)
+
+
+def _formula(c):
+    i = np.arange(c["rot_dim"] // 2)
+    f = c["theta"] ** (-2.0 * i / c["rot_dim"])
+    if c.get("scaling") == "linear":
+        return f / c["factor"]
+    if c.get("scaling") == "bands":
+        wavelength = 2.0 * math.pi / f
+        g = np.clip((c["orig_len"] / wavelength - c["band_low"]) / (c["band_high"] - c["band_low"]), 0, 1)
+        return g * f + (1 - g) * f / c["factor"]
+    return f
+
+
+@pytest.mark.parametrize("cfg", [PLAIN, dict(PLAIN, rot_dim=2), dict(PLAIN, rot_dim=256, theta=5.0e5),
+                                 dict(PLAIN, scaling="linear", factor=8.0), BANDS,
+                                 dict(BANDS, band_high=4.0, factor=32.0, rot_dim=80)])
+def test_rope_frequencies_follow_the_formula(zo, cfg):
+    got = zo.zo_rope_frequencies(cfg)
+    # pow, two products and a division in fp64: a handful of half steps of 2^-53
+    np.testing.assert_allclose(got, _formula(cfg), rtol=16 * 2.0 ** -53, atol=0)
+
+
+def test_rope_bands_keep_fast_and_interpolate_slow_frequencies(zo):
+    plain = zo.zo_rope_frequencies(dict(theta=BANDS["theta"], rot_dim=128))
+    scaled = zo.zo_rope_frequencies(BANDS)
+    turns = BANDS["orig_len"] * plain / (2 * math.pi)
+    assert np.array_equal(scaled[turns >= 32], plain[turns >= 32])
+    assert np.array_equal(scaled[turns <= 1], plain[turns <= 1] / 4.0)
+    assert np.all(np.diff(scaled) < 0)
+
+
+@pytest.mark.parametrize("bad", [dict(theta=0.0), dict(theta=-1.0), dict(theta=math.inf), dict(theta=math.nan),
+                                 dict(rot_dim=0), dict(rot_dim=3), dict(rot_dim=258), dict(rot_dim=-2),
+                                 dict(scaling=7), dict(scaling="linear", factor=0.0),
+                                 dict(scaling="linear", factor=math.nan),
+                                 dict(scaling="bands", factor=2.0, orig_len=0.0, band_low=1.0, band_high=4.0),
+                                 dict(scaling="bands", factor=2.0, orig_len=64.0, band_low=4.0, band_high=4.0),
+                                 dict(magnitude=math.inf)])
+def test_rope_configuration_refusals(zo, bad):
+    with pytest.raises(zo.ZoError) as e:
+        zo.zo_rope_frequencies({**PLAIN, **bad})
+    assert e.value.status == zo.ZO_ERR_INVALID
+
+
+def test_rope_interleaved_must_be_zero_or_one(zo):
+    c = zo.zo_rope_cfg.from_dict(PLAIN)
+    c.interleaved = 2
+    out = np.zeros(32)
+    assert zo.lib.zo_rope_frequencies(ctypes.byref(c), out.ctypes.data) == zo.ZO_ERR_INVALID
+    assert zo.lib.zo_rope_frequencies(None, out.ctypes.data) == zo.ZO_ERR_INVALID
+    assert zo.lib.zo_rope_frequencies(ctypes.byref(zo.zo_rope_cfg.from_dict(PLAIN)), None) == zo.ZO_ERR_INVALID
+
+
+def test_null_contexts_are_refused(zo):
+    c = zo.zo_rope_cfg.from_dict(PLAIN)
+    L = zo.lib
+    assert L.zo_rope(None, 16, 32, 0, None, ctypes.byref(c), 1, 64, 64, 1, 64) == zo.ZO_ERR_INVALID
+    assert L.zo_attention_packed(None, 16, 16, 16, 16, 16, 1, 1, 64, 64, 64, 64, 1, 1, 64, 1.0) == zo.ZO_ERR_INVALID
+    assert L.zo_logprobs(None, 16, 0, 1, 8, 8, 16, 16, 16, 0, None, None) == zo.ZO_ERR_INVALID
+    assert L.zo_head_logprobs(None, 16, 16, 1, 8, 8, 8, 8, 16, 16, 16, 16, 1 << 20) == zo.ZO_ERR_INVALID
+
+
+@pytest.mark.parametrize("rows,vocab", [(0, 8), (-1, 8), (1, 0), (1 << 31, 8), (1, 1 << 31)])
+def test_head_workspace_refusals(zo, rows, vocab):
+    with pytest.raises(zo.ZoError):
+        zo.zo_head_logprobs_workspace(rows, vocab)
+    n = ctypes.c_int64(-7)
+    assert zo.lib.zo_head_logprobs_workspace(rows, vocab, ctypes.byref(n)) == zo.ZO_ERR_INVALID
+    assert n.value == -7
+    assert zo.lib.zo_head_logprobs_workspace(1, 8, None) == zo.ZO_ERR_INVALID
+
+
+@pytest.mark.parametrize("vocab", [1, 31, 32, 1000, 50272, 151936])
+def test_head_workspace_is_far_below_the_logits(zo, vocab):
+    """It grows with the rows, and at large vocabularies stays far below rows x vocab fp32."""
+    last = 0
+    for rows in (1, 127, 128, 129, 1000, 4096, 20000):
+        n = zo.zo_head_logprobs_workspace(rows, vocab)
+        assert n > 0 and n % 4 == 0
+        if vocab >= 50272:
+            assert n < rows * vocab * 4 // 32
+        last = max(last, n)
+    assert last == n
+
+
+def _find_tile(cu, total, slot):
+    """find_tile of the packed attention: (first row, length, query tile) or length 0."""
+    base = 0
+    for s, e in zip(cu[:-1], cu[1:]):
+        if s < 0 or e < s or e > total:
+            s = e = 0
+        n = (e - s + 127) // 128
+        if base + n > slot:
+            return s, e - s, slot - base
+        base += n
+    return 0, 0, 0
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 5], [128, 129, 127], [1] * 300, [0, 1000, 0, 1, 2]])
+@pytest.mark.parametrize("extra", [0, 5])
+def test_every_query_row_is_in_exactly_one_block(lens, extra):
+    """ceil(total / 128) + n_seqs blocks cover every tile of every sequence once."""
+    cu = [0] + np.cumsum(lens).tolist()
+    total = max(1, cu[-1] + extra)
+    seen = np.zeros(total, int)
+    for slot in range((total + 127) // 128 + len(lens)):
+        row0, n, qt = _find_tile(cu, total, slot)
+        if n:
+            seen[row0 + 128 * qt: row0 + min(n, 128 * qt + 128)] += 1
+    assert np.all(seen[: cu[-1]] == 1) and np.all(seen[cu[-1]:] == 0)
+
+
+@pytest.mark.parametrize("cu", [[0, 10, 5, 20], [-3, 10, 20], [0, 10, 40], [2 ** 31 - 1, -2 ** 31, 4]])
+def test_bad_offsets_never_leave_the_buffer(cu):
+    total = 32
+    for slot in range(1 + len(cu)):
+        row0, n, qt = _find_tile(cu, total, slot)
+        assert 0 <= row0 and row0 + n <= total

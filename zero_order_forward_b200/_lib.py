@@ -23,11 +23,15 @@ ZO_F32, ZO_BF16 = 0, 1
  ZO_ERR_UNSUPPORTED, ZO_ERR_TIMEOUT) = range(8)
 ZO_FLAG_NONFINITE = 0x1
 ZO_FLAG_TIMEOUT = 0x2
+ZO_FLAG_OFFSETS = 0x4
 ZO_EPI_BIAS_BF16, ZO_EPI_RELU_BF16, ZO_EPI_RESID_F32 = 0, 1, 2
 ZO_KT_GEMM, ZO_KT_ATTENTION, ZO_KT_PERTURB, ZO_KT_UPDATE, ZO_KT_COUNT = 0, 1, 2, 3, 4
 KERNEL_CLASSES = ("gemm", "attention", "perturb", "update")
 ZO_MAX_PROBES = 1024
 ZO_NOALLOC_MAX_BATCH = 4096
+ZO_ROPE_PLAIN, ZO_ROPE_LINEAR, ZO_ROPE_BANDS = 0, 1, 2
+ZO_ROPE_MAX_HEAD_DIM = 256
+ZO_MAX_TOP = 32
 
 _vp, _i32, _i64, _u32, _u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
 _f32, _f64, _int = ctypes.c_float, ctypes.c_double, ctypes.c_int
@@ -81,6 +85,13 @@ _SIGS = {
     "zo_kernel_times": [_vp, _vp, ctypes.POINTER(_i64)],
     "zo_launch_count": [_vp, ctypes.POINTER(_i64)],
     "zo_set_loss_location": [_vp, _int],
+    "zo_rope_frequencies": [_vp, _vp],
+    "zo_rope": [_vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _i32, _i32],
+    "zo_attention_packed": [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32,
+                            _i32, _i32, _f32],
+    "zo_logprobs": [_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp],
+    "zo_head_logprobs_workspace": [_i64, _i64, ctypes.POINTER(_i64)],
+    "zo_head_logprobs": [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64],
     "zo_model_step_host": [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _f32, _f32, _f32, _int, _vp],
 }
 for _name, _args in _SIGS.items():
@@ -459,6 +470,90 @@ def zo_rmsnorm(ctx, x, w, out, rows, d, eps):
 def zo_layernorm(ctx, x, gamma, beta, out, rows, d):
     return ctx.check(_L.zo_layernorm(ctx.handle, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(out),
                                      rows, d))
+
+
+# ------------------------------------------------------------------ packed prompts
+
+
+ROPE_SCALINGS = {"none": ZO_ROPE_PLAIN, "linear": ZO_ROPE_LINEAR, "bands": ZO_ROPE_BANDS}
+
+
+class zo_rope_cfg(ctypes.Structure):
+    _fields_ = [("theta", _f32), ("rot_dim", _i32), ("interleaved", _i32), ("scaling", _i32),
+                ("factor", _f32), ("orig_len", _f32), ("band_low", _f32), ("band_high", _f32),
+                ("magnitude", _f32)]
+
+    @classmethod
+    def from_dict(cls, c):
+        scaling = c.get("scaling", "none")
+        return cls(float(c["theta"]), int(c["rot_dim"]), int(bool(c.get("interleaved", False))),
+                   ROPE_SCALINGS.get(scaling, scaling), float(c.get("factor", 1.0)),
+                   float(c.get("orig_len", 0.0)), float(c.get("band_low", 0.0)),
+                   float(c.get("band_high", 0.0)), float(c.get("magnitude", 1.0)))
+
+
+def _rope_cfg(cfg):
+    return cfg if isinstance(cfg, zo_rope_cfg) else zo_rope_cfg.from_dict(cfg)
+
+
+def _dtype(t, dtype):
+    """ZO_F32 / ZO_BF16 of a tensor, unless given."""
+    if dtype is not None:
+        return int(dtype)
+    import torch
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{t.dtype}: float32 or bfloat16 expected")
+    return ZO_F32 if t.dtype == torch.float32 else ZO_BF16
+
+
+def zo_rope_frequencies(cfg):
+    """The rot_dim / 2 angular frequencies of a zo_rope_cfg (or dict), radians per position."""
+    import numpy as np
+    c = _rope_cfg(cfg)
+    out = np.zeros(max(0, min(c.rot_dim, ZO_ROPE_MAX_HEAD_DIM)) // 2, np.float64)
+    st = _L.zo_rope_frequencies(ctypes.byref(c), out.ctypes.data)
+    if st != ZO_OK:
+        raise ZoError(st, "invalid rotary configuration")
+    return out
+
+
+def zo_rope(ctx, x, out, positions, cfg, rows, ldx, ldo, n_heads, head_dim, dtype=None):
+    """cfg: a zo_rope_cfg, or a dict of its fields (scaling "none", "linear" or "bands")."""
+    return ctx.check(_L.zo_rope(ctx.handle, _ptr(x), _ptr(out), _dtype(x, dtype), _ptr(positions),
+                                ctypes.byref(_rope_cfg(cfg)), rows, ldx, ldo, n_heads, head_dim))
+
+
+def zo_attention_packed(ctx, q, k, v, out, cu_seqlens, n_seqs, total_tokens, ldq, ldk, ldv, ldo,
+                        n_heads, n_kv_heads, head_dim, scale):
+    return ctx.check(_L.zo_attention_packed(ctx.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                            _ptr(cu_seqlens), n_seqs, total_tokens, ldq, ldk, ldv,
+                                            ldo, n_heads, n_kv_heads, head_dim, scale))
+
+
+def zo_logprobs(ctx, logits, rows, vocab, ld, targets, logprob, entropy, top=0, top_ids=None,
+                top_logprobs=None, dtype=None):
+    return ctx.check(_L.zo_logprobs(ctx.handle, _ptr(logits), _dtype(logits, dtype), rows, vocab, ld,
+                                    _ptr(targets), _ptr(logprob), _ptr(entropy), top, _ptr(top_ids),
+                                    _ptr(top_logprobs)))
+
+
+def zo_head_logprobs_workspace(rows, vocab):
+    """Bytes of workspace that zo_head_logprobs needs."""
+    n = _i64()
+    st = _L.zo_head_logprobs_workspace(rows, vocab, ctypes.byref(n))
+    if st != ZO_OK:
+        raise ZoError(st, "invalid sizes")
+    return n.value
+
+
+def zo_head_logprobs(ctx, hidden, W, rows, vocab, width, ldh, ldw, targets, logprob, entropy,
+                     workspace, workspace_bytes=None):
+    """workspace: a device tensor (its size is taken) or an address with workspace_bytes."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return ctx.check(_L.zo_head_logprobs(ctx.handle, _ptr(hidden), _ptr(W), rows, vocab, width, ldh,
+                                         ldw, _ptr(targets), _ptr(logprob), _ptr(entropy),
+                                         _ptr(workspace), workspace_bytes))
 
 
 def zo_enable_phase_timing(ctx, n_steps):

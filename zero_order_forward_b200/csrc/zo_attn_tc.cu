@@ -77,53 +77,12 @@ struct TcAttnArgs {
   uint32_t *err;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
-  return pack_bf16x2(lo, hi);
-}
-
-// max(a, b, c): one three-input instruction instead of two.
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// Two lanes of fp32 arithmetic per instruction (sm_100's packed f32x2 forms), each lane
-// rounded exactly as the scalar instruction: (d0, d1) = (a0 * b + c, a1 * b + c).
-__device__ __forceinline__ void fma2_bc(float a0, float a1, float b, float c, float &d0, float &d1) {
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-// (s0, s1) += (a0, a1)
-__device__ __forceinline__ void add2(float &s0, float &s1, float a0, float a1) {
-  asm("{\n\t.reg .b64 s, a;\n\t"
-      "mov.b64 s, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\t"
-      "add.rn.f32x2 s, s, a;\n\tmov.b64 {%0, %1}, s;\n\t}"
-      : "+f"(s0), "+f"(s1) : "f"(a0), "f"(a1));
-}
-
-// All lanes of the warp wait for `parity` on `bar`: lane 0 decides (bounded), then every lane
-// observes the completed phase.  Returns false (on every lane) on expiry or abort.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  const int lane = threadIdx.x & 31;
-  int ok = 1;
-  if (lane == 0) ok = (!*abort_flag && tc::mbar_wait(bar, parity)) ? 1 : 0;
-  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-  if (ok && lane != 0) ok = tc::mbar_wait(bar, parity) ? 1 : 0;
-  return __all_sync(0xFFFFFFFFu, ok) != 0;
-}
-
-// Phase bookkeeping of a ring of `n` barriers used once per item i: item i uses barrier
-// i % n, and its completion is phase i / n of that barrier.
-__device__ __forceinline__ uint32_t ring_parity(int i, int n) { return (uint32_t)(i / n) & 1u; }
+using tc::add2;
+using tc::ex2;
+using tc::fma2_bc;
+using tc::max3f;
+using tc::ring_parity;
+using tc::warp_wait;
 
 template <int HD>
 __global__ void __launch_bounds__(kTThreads, TcAttnCfg<HD>::kCtas)
@@ -309,7 +268,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         const float p0 = ex2(x0), p1 = ex2(x1);
         if ((c >> 1) & 1) add2(ls4[2], ls4[3], p0, p1);
         else add2(ls4[0], ls4[1], p0, p1);
-        pk[c / 2] = pack2_bf16(p0, p1);
+        pk[c / 2] = pack_bf16x2(p0, p1);
       }
       const float lsum = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
       if (__any_sync(0xFFFFFFFFu, need)) {
@@ -346,10 +305,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         if (r < a.S) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 w = make_uint4(pack2_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
-                                       pack2_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                       pack2_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                       pack2_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+            const uint4 w = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv),
+                                       pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                       pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                                       pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
             *reinterpret_cast<uint4 *>(orow + 32 * c + 8 * q) = w;
           }
         }

@@ -379,6 +379,8 @@ zo_status zo_sync(zo_ctx *ctx, uint32_t *flags) {
   }
   if (flags) *flags = s.flags;
   if (s.flags & ZO_FLAG_TIMEOUT) return fail(ctx, ZO_ERR_TIMEOUT, "a kernel gave up a bounded wait");
+  if (s.flags & ZO_FLAG_OFFSETS)
+    return fail(ctx, ZO_ERR_INVALID, "sequence offsets decreased or left their buffer; sequences skipped");
   if (s.flags & ZO_FLAG_NONFINITE) return fail(ctx, ZO_ERR_NONFINITE, "a loss was not finite; step skipped");
   return ZO_OK;
 }

@@ -682,6 +682,14 @@ bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int 
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+bool tile_map_bf16(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  return make_map(m, base, rows, cols, box_rows, ld);
+}
+
+namespace {
+
 template <int BN, int STAGES, int EPI, bool PERT = false>
 cudaError_t launch_one(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tcm,
                        const GemmArgs &g, cudaStream_t st, const ProbeKey &pk = ProbeKey{},

@@ -1,0 +1,356 @@
+// zo_head.cu -- log probabilities of given tokens and entropy straight from hidden states and
+// the head matrix (zo_head_logprobs): for x[r][j] = hidden[r] . W[j],
+//
+//   lse_r = log sum_j exp(x_rj),  logprob_r = x_{r,t} - lse_r,  H_r = lse_r - sum_j p_rj x_rj,
+//
+// without the [rows][vocab] logits in memory.  The product runs on the tensor cores as in
+// zo_gemm.cu (TMA ring, tcgen05.mma, fp32 accumulators in tensor memory); instead of storing the
+// accumulator, the epilogue threads, one row each, keep m (largest logit times log2 e),
+// s = sum 2^(x log2 e - m) and u = sum 2^(x log2 e - m) (x log2 e - m) over all columns that
+// they see, and write one triple per row at the end.  A second kernel joins a row's triples in a
+// fixed order.
+//
+// One CTA takes 128 rows and a contiguous range of W's rows in units of 32 (so that the ranges of
+// 148 CTAs differ by one unit, not by one 256-row tile), 256 at a time; the last tile of a range
+// may be narrower (the MMA's N and the number of loaded boxes follow).
+#include <cmath>
+
+#include "zo_internal.cuh"
+#include "zo_tc.cuh"
+
+namespace zo {
+namespace {
+
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr double kLn2 = 0.69314718055994530942;
+constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
+constexpr int kUnit = 32;  // rows of W in one TMA box, and the unit of a CTA's range
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+
+struct HeadSmem {
+  static constexpr uint32_t kABytes = kBM * kBK * 2;
+  static constexpr uint32_t kBBytes = kBN * kBK * 2;
+  static constexpr uint32_t kBoxBytes = kUnit * kBK * 2;
+  static constexpr uint32_t kBarOffset = kStages * (kABytes + kBBytes);
+  static constexpr uint32_t kBytes = kBarOffset + 256 + 1024;
+  static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barrier area");
+};
+
+struct HeadArgs {
+  int rows, vocab, width;
+  int splits;             // ranges of W's rows
+  int units;              // ceil(vocab / kUnit)
+  const int32_t *targets; // may be null
+  float4 *part;           // [rows][2 splits] (m, s, u, -)
+  float *target_logit;    // [rows]
+  uint32_t *err;
+};
+
+// Rows of W of range i: [first, last), whole units except at the end of the vocabulary.
+__host__ __device__ __forceinline__ int range_first(int i, int units, int splits) {
+  return (int)((int64_t)units * i / splits) * kUnit;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, HeadArgs a) {
+  using S = HeadSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sA = smem, *sB = smem + kStages * S::kABytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBarOffset);
+  uint64_t *empty = full + kStages;
+  uint64_t *acc_full = empty + kStages;  // [2]
+  uint64_t *acc_empty = acc_full + 2;    // [2]
+  uint64_t *mma_done = acc_empty + 2;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = blockIdx.x * kBM, split = blockIdx.y;
+  const int n_first = range_first(split, a.units, a.splits);
+  const int n_last = min(range_first(split + 1, a.units, a.splits), a.vocab);
+  const int tiles = (n_last - n_first + kBN - 1) / kBN;
+  const int nk = (a.width + kBK - 1) / kBK;
+  // loaded rows of a tile: whole units (rows past the vocabulary read as zero and are masked)
+  auto tile_units = [&](int t) { return min(kBN / kUnit, (n_last - n_first - t * kBN + kUnit - 1) / kUnit); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&acc_full[b], 1);
+      tc::mbar_init(&acc_empty[b], kEpiWarps);
+    }
+    tc::mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_holder, 2 * kBN);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  uint32_t issued = 0;
+  if (warp == 0 && lane == 0) {
+    tc::tma_prefetch_desc(&tmA);
+    tc::tma_prefetch_desc(&tmB);
+    for (int t = 0; t < tiles && !*abort_flag; ++t) {
+      const int boxes = tile_units(t);
+      for (int kb = 0; kb < nk; ++kb) {
+        const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
+        if (*abort_flag || !tc::mbar_wait(&empty[s], ph ^ 1u)) {
+          atomicOr(a.err, ZO_FLAG_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        tc::mbar_arrive_expect_tx(&full[s], S::kABytes + (uint32_t)boxes * S::kBoxBytes);
+        tc::tma_load_2d(sA + s * S::kABytes, &tmA, &full[s], kb * kBK, m0);
+        for (int b = 0; b < boxes; ++b)
+          tc::tma_load_2d(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, &full[s], kb * kBK,
+                          n_first + t * kBN + b * kUnit);
+        ++issued;
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    uint32_t consumed = 0;
+    for (int t = 0; t < tiles && !*abort_flag; ++t) {
+      const int b = t & 1;
+      if (!tc::mbar_wait(&acc_empty[b], ((uint32_t)(t >> 1) & 1u) ^ 1u)) {
+        atomicOr(a.err, ZO_FLAG_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      tc::tc_fence_after();
+      const uint32_t idesc = tc::idesc_bf16_f32(kBM, tile_units(t) * kUnit);
+      const uint32_t d = tmem + (uint32_t)(b * kBN);
+      for (int kb = 0; kb < nk; ++kb) {
+        const uint32_t s = consumed % kStages, ph = (consumed / kStages) & 1u;
+        if (*abort_flag || !tc::mbar_wait(&full[s], ph)) {
+          atomicOr(a.err, ZO_FLAG_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t a0 = tc::smem_addr(sA + s * S::kABytes);
+        const uint32_t b0 = tc::smem_addr(sB + s * S::kBBytes);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          tc::mma_bf16(d, tc::smem_desc_k128(a0 + 32 * k), tc::smem_desc_k128(b0 + 32 * k), idesc,
+                       (kb | k) != 0 ? 1u : 0u);
+        tc::mma_commit(&empty[s]);
+        ++consumed;
+      }
+      if (*abort_flag) break;
+      tc::mma_commit(&acc_full[b]);
+    }
+    tc::mma_commit(mma_done);  // arrives once every MMA issued above has retired
+  } else if (warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) / 4;  // TMEM lane quadrant; half of the columns
+    const int row = m0 + 32 * q + lane;
+    const int target = a.targets && row < a.rows ? a.targets[row] : -1;
+    float m = -INFINITY, s = 0.f, u = 0.f;
+    bool ok = true;
+    for (int t = 0; t < tiles; ++t) {
+      const int b = t & 1;
+      int w = 1;
+      if (lane == 0) w = (!*abort_flag && tc::mbar_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u)) ? 1 : 0;
+      w = __shfl_sync(0xFFFFFFFFu, w, 0);
+      if (w && lane != 0) w = tc::mbar_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u) ? 1 : 0;
+      if (!__all_sync(0xFFFFFFFFu, w)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const int n0 = n_first + t * kBN, cols = min(kBN, n_last - n0);
+      const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+      for (int c0 = half * (kBN / 2); c0 < min(cols, (half + 1) * (kBN / 2)); c0 += 32) {
+        float v[32];
+        tc::tmem_ld32(base + (uint32_t)c0, v);
+        const int hit = target - (n0 + c0);
+        if (__any_sync(0xFFFFFFFFu, hit >= 0 && hit < 32)) {
+          float x = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x = i == hit ? v[i] : x;
+          if (hit >= 0 && hit < min(32, cols - c0)) a.target_logit[row] = x;
+        }
+        if (c0 + 32 > cols) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = c0 + i < cols ? v[i] : -1e30f;
+        }
+        float mx = v[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) mx = fmaxf(mx, v[i]);
+        mx *= kLog2E;
+        if (mx > m) {
+          if (m != -INFINITY) {
+            const float d = m - mx, e = tc::ex2(d);
+            u = e * (u + d * s);
+            s *= e;
+          }
+          m = mx;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float x = fmaf(v[i], kLog2E, -m), p = tc::ex2(x);
+          s += p;
+          u = fmaf(p, x, u);
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&acc_empty[b]);
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.err, ZO_FLAG_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (row < a.rows)
+      a.part[(int64_t)row * (2 * a.splits) + 2 * split + half] = make_float4(m, s, u, 0.f);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    // let this CTA's TMA loads still in flight land before it exits (bounded)
+    for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
+      if (issued <= s) continue;
+      const uint32_t last = s + ((issued - 1 - s) / kStages) * kStages;
+      if (!tc::mbar_wait(&full[s], (last / kStages) & 1u)) atomicOr(a.err, ZO_FLAG_TIMEOUT);
+    }
+  }
+  if (warp == 1) {
+    if (lane == 0 && !tc::mbar_wait(mma_done, 0)) atomicOr(a.err, ZO_FLAG_TIMEOUT);
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 2 * kBN);
+  }
+}
+
+// One warp per row: its triples joined lane by lane, then across the lanes.
+__global__ void __launch_bounds__(256)
+head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= a.rows) return;
+  const float4 *part = a.part + (int64_t)row * (2 * a.splits);
+  float m = -INFINITY;
+  for (int i = lane; i < 2 * a.splits; i += 32) m = fmaxf(m, part[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float s = 0.f, u = 0.f;
+  for (int i = lane; i < 2 * a.splits; i += 32) {
+    const float4 t = part[i];
+    const float d = t.x - m, e = tc::ex2(d);
+    if (t.x != -INFINITY) {  // a half tile that held no column has none
+      s += e * t.y;
+      u += e * (t.z + d * t.y);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+  }
+  if (lane != 0) return;
+  const double log2s = log2((double)s);
+  if (entropy) entropy[row] = (float)(kLn2 * (log2s - (double)u / (double)s));
+  if (logprob) {
+    const int32_t t = a.targets[row];
+    float v = __uint_as_float(0x7FC00000u);
+    if (t == -1) v = 0.f;
+    else if (t >= 0 && t < a.vocab)
+      v = (float)(kLn2 * ((double)a.target_logit[row] * (double)kLog2E - (double)m - log2s));
+    logprob[row] = v;
+  }
+}
+
+// Ranges of W's rows for `rows` rows: one CTA of every SM for up to 128 rows, then the smallest
+// count that fills whole waves of the 148 SMs to 97% (at most 32 per row tile).
+int head_splits(int64_t rows, int64_t vocab) {
+  const int64_t units = (vocab + kUnit - 1) / kUnit, m = (rows + kBM - 1) / kBM;
+  int64_t best = 1;
+  double fill = 0.0;
+  const int64_t most = m * 32 < kSmCount ? kSmCount / m : 32;
+  for (int64_t s = 1; s <= most && s <= units; ++s) {
+    const double waves = (double)(m * s) / kSmCount, f = waves / std::ceil(waves);
+    if (f > fill + 1e-9) {
+      fill = f;
+      best = s;
+    }
+    if (m > 1 && fill >= 0.97) break;
+  }
+  return (int)best;
+}
+
+bool head_sizes_ok(int64_t rows, int64_t vocab) {
+  return rows >= 1 && rows < INT32_MAX - 256 && vocab >= 1 && vocab < INT32_MAX - 512;
+}
+
+int64_t head_bytes(int64_t rows, int64_t vocab) {
+  return rows * (2 * (int64_t)head_splits(rows, vocab) * (int64_t)sizeof(float4)) + ((rows * 4 + 15) / 16) * 16;
+}
+
+}  // namespace
+}  // namespace zo
+
+using namespace zo;
+
+extern "C" {
+
+zo_status zo_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t *bytes) {
+  if (!bytes || !head_sizes_ok(rows, vocab)) return ZO_ERR_INVALID;
+  *bytes = head_bytes(rows, vocab);
+  return ZO_OK;
+}
+
+zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64_t rows, int64_t vocab,
+                           int64_t width, int64_t ldh, int64_t ldw, const int32_t *targets,
+                           float *logprob, float *entropy, void *workspace, int64_t workspace_bytes) {
+  if (!ctx) return ZO_ERR_INVALID;
+  ctx->err.clear();
+  if (!hidden || !W || !workspace || (logprob && !targets) || (!logprob && !entropy))
+    return fail(ctx, ZO_ERR_INVALID, "null head_logprobs argument");
+  if (!head_sizes_ok(rows, vocab) || width < 1 || width >= INT32_MAX - 64 || width % 8 || ldh < width ||
+      ldw < width || ldh > INT32_MAX || ldw > INT32_MAX || ldh % 8 || ldw % 8)
+    return fail(ctx, ZO_ERR_INVALID, "head_logprobs: need rows, vocab, width >= 1 (below 2^31), width, ldh "
+                "and ldw multiples of 8, ldh and ldw >= width");
+  if ((reinterpret_cast<uintptr_t>(hidden) | reinterpret_cast<uintptr_t>(W) |
+       reinterpret_cast<uintptr_t>(workspace)) & 15u)
+    return fail(ctx, ZO_ERR_INVALID, "head_logprobs: hidden, W and the workspace must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(targets) | reinterpret_cast<uintptr_t>(logprob) |
+       reinterpret_cast<uintptr_t>(entropy)) % 4)
+    return fail(ctx, ZO_ERR_INVALID, "head_logprobs: pointers not aligned to their elements");
+  if (workspace_bytes < head_bytes(rows, vocab))
+    return fail(ctx, ZO_ERR_INVALID, "head_logprobs: workspace of %lld bytes, %lld needed",
+                (long long)workspace_bytes, (long long)head_bytes(rows, vocab));
+  const DeviceScope device(ctx);
+  if (device.status != cudaSuccess)
+    return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
+  CUtensorMap ta, tb;
+  if (!tile_map_bf16(&ta, hidden, rows, width, ldh, kBM) || !tile_map_bf16(&tb, W, vocab, width, ldw, kUnit))
+    return fail(ctx, ZO_ERR_CUDA, "head_logprobs: cuTensorMapEncodeTiled failed");
+  HeadArgs a;
+  a.rows = (int)rows;
+  a.vocab = (int)vocab;
+  a.width = (int)width;
+  a.splits = head_splits(rows, vocab);
+  a.units = (int)((vocab + kUnit - 1) / kUnit);
+  a.targets = targets;
+  a.part = static_cast<float4 *>(workspace);
+  a.target_logit = reinterpret_cast<float *>(a.part + rows * 2 * a.splits);
+  a.err = &ctx->dstate->flags;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(head_kernel), (int)HeadSmem::kBytes);
+  if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_kernel attribute: %s", cudaGetErrorString(e));
+  const dim3 grid((unsigned)((rows + kBM - 1) / kBM), (unsigned)a.splits);
+  head_kernel<<<grid, kThreads, HeadSmem::kBytes, ctx->stream>>>(ta, tb, a);
+  zo_status st = check_launch(ctx, "head_kernel");
+  if (st != ZO_OK) return st;
+  head_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, ctx->stream>>>(a, logprob, entropy);
+  return check_launch(ctx, "head_join_kernel");
+}
+
+}  // extern "C"

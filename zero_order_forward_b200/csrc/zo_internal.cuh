@@ -239,6 +239,22 @@ void ktime_end(zo_ctx *ctx, int slot, int cls, double work);
 zo_status step_device(zo_ctx *ctx, const double *loss_plus, const double *loss_minus, int32_t n_pert,
                       const double *loss0, float lr, float eps, float damping);
 
+// Makes a context's device current for a call and puts the caller's back at its end.
+struct DeviceScope {
+  explicit DeviceScope(const zo_ctx *ctx) {
+    if (cudaGetDevice(&before) != cudaSuccess) before = -1;
+    if (before != ctx->device) status = cudaSetDevice(ctx->device);
+  }
+  ~DeviceScope() {
+    int now = -1;
+    if (before >= 0 && cudaGetDevice(&now) == cudaSuccess && now != before) cudaSetDevice(before);
+  }
+  DeviceScope(const DeviceScope &) = delete;
+  DeviceScope &operator=(const DeviceScope &) = delete;
+  int before = -1;
+  cudaError_t status = cudaSuccess;
+};
+
 // Launchers (each enqueues on ctx->stream and returns the launch status).
 zo_status launch_perturb(zo_ctx *ctx, const ProbeKey &pk, int64_t first, int64_t count,
                          void *out);

@@ -9,6 +9,11 @@
 #include <stdint.h>
 
 namespace zo {
+
+// Tensor map of a row-major bf16 matrix [rows][cols], ld elements between row starts, read in
+// boxes of box_rows rows x 64 columns with the 128-byte swizzle (zero outside the matrix).
+bool tile_map_bf16(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
+
 namespace tc {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
@@ -86,6 +91,52 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     if ((i & 15u) == 0u && globaltimer() - t0 > kWaitLimitNs) return false;
   }
 }
+
+// ------------------------------------------------------------------ arithmetic
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// max(a, b, c): one three-input instruction instead of two.
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two lanes of fp32 arithmetic per instruction (sm_100's packed f32x2 forms), each lane
+// rounded exactly as the scalar instruction: (d0, d1) = (a0 * b + c, a1 * b + c).
+__device__ __forceinline__ void fma2_bc(float a0, float a1, float b, float c, float &d0, float &d1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+// (s0, s1) += (a0, a1)
+__device__ __forceinline__ void add2(float &s0, float &s1, float a0, float a1) {
+  asm("{\n\t.reg .b64 s, a;\n\t"
+      "mov.b64 s, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, a;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1) : "f"(a0), "f"(a1));
+}
+
+// All lanes of the warp wait for `parity` on `bar`: lane 0 decides (bounded), then every lane
+// observes the completed phase.  Returns false (on every lane) on expiry or abort.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+  const int lane = threadIdx.x & 31;
+  int ok = 1;
+  if (lane == 0) ok = (!*abort_flag && mbar_wait(bar, parity)) ? 1 : 0;
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  if (ok && lane != 0) ok = mbar_wait(bar, parity) ? 1 : 0;
+  return __all_sync(0xFFFFFFFFu, ok) != 0;
+}
+
+// Phase bookkeeping of a ring of `n` barriers used once per item i: item i uses barrier
+// i % n, and its completion is phase i / n of that barrier.
+__device__ __forceinline__ uint32_t ring_parity(int i, int n) { return (uint32_t)(i / n) & 1u; }
 
 // ------------------------------------------------------------------ programmatic dependent launch
 
