@@ -3,17 +3,18 @@
 //
 //   p_j = exp(x_j - lse),  lse = log sum_j exp(x_j),  logprob = x_t - lse,  H = lse - sum_j p_j x_j.
 //
-// One block per row.  Every thread keeps, over the 16-byte vectors that it reads, a reference m
-// (the largest logit so far times log2 e), s = sum 2^(x log2 e - m) and
-// u = sum 2^(x log2 e - m) (x log2 e - m); a larger maximum rescales both.  The block joins the
-// threads' triples in a fixed order, so that H = ln 2 (log2 s - u / s) and
-// logprob = ln 2 (x_t log2 e - m - log2 s); the logarithms are fp64, once per row.
+// A row is one block's, or, where rows are few, a cluster's of up to 8 blocks.  Every thread keeps,
+// over the 16-byte vectors that it reads, m (its largest logit so far), s = sum 2^t and
+// u = sum 2^t t with t = (x - m) log2 e; a larger maximum rescales both.  The triples are joined
+// in a fixed order, so that H = ln 2 (log2 s - u / s) and logprob = (x_t - m) - ln 2 log2 s; the
+// logarithm and the last sums are fp64, once per row.  The difference x - m is taken before the
+// scaling, so that rows of huge logits lose and overflow nothing.
 //
 // Alternatives: a thread also keeps which of its vectors holds its largest logit first.  The
-// top-th largest of the threads' (value, vector) keys is a bound that at least `top` logits of
-// the row reach, and only threads whose own key reaches it can hold such logits: their vectors
-// are read again (from L2) and what reaches the bound is sorted.  Keys are unique, so equal
-// logits come in the order of their index.
+// top-th largest of the block's (value, vector) keys is a bound that at least `top` of its logits
+// reach, and only threads whose own key reaches it can hold such logits: their vectors are read
+// again (from L2) and what reaches the bound is sorted.  Keys are unique, so equal logits come
+// in the order of their index.
 #include <cmath>
 
 #include "zo_internal.cuh"
@@ -24,17 +25,14 @@ namespace {
 
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
-// Logits below -kLowest count as that in the fast sums: 2^(x log2 e - m) is 0 all the same, and
-// 0 (x log2 e - m) stays 0 (not 0 * inf).  The rounding of m cancels, but 2^ of it must stay in
-// range: a row whose largest logit is kHuge or more in magnitude takes the exact form
-// (row_stats_huge), and a thread whose own largest is -kHuge or less adds nothing.
-constexpr float kLowest = 1e30f, kHuge = 1e8f;
-constexpr int kCandidates = 1024;  // logits that may reach the bound before the slow selection
+// t below -kLowest (a masked logit's is -inf) counts as that: 2^t is 0 all the same, and 0 t stays 0.
+constexpr float kLowest = 1e30f;
+constexpr int kMaxSplits = 8;  // blocks of a row (a portable cluster)
 
 struct LogprobArgs {
   const void *logits;
   int64_t ld;
-  int vocab, top;
+  int vocab, top, splits;
   const int32_t *targets;
   float *logprob, *entropy;
   int32_t *top_ids;
@@ -66,23 +64,45 @@ __device__ __forceinline__ uint32_t index_of(uint64_t key) { return 0xFFFFFFFEu 
 template <typename T> struct Row;
 template <> struct Row<float> {
   static constexpr int kVec = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;  // -inf, in every element of a 32-bit word
   static __device__ __forceinline__ float one(const float *p) { return __ldg(p); }
-  static __device__ __forceinline__ void vec(const float *p, float f[4]) {
-    const float4 r = __ldg(reinterpret_cast<const float4 *>(p));
-    f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+  static __device__ __forceinline__ void set(uint4 &r, int i, const float *p) {
+    (&r.x)[i] = __float_as_uint(__ldg(p));
+  }
+  static __device__ __forceinline__ void open(const uint4 &r, float f[4]) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+  }
+  // The largest element, NaN if there is one.
+  static __device__ __forceinline__ float largest(const uint4 &r) {
+    return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
+                   max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
 };
 template <> struct Row<uint16_t> {
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;
   static __device__ __forceinline__ float one(const uint16_t *p) { return bf16_bits_to_f32(__ldg(p)); }
-  static __device__ __forceinline__ void vec(const uint16_t *p, float f[8]) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
+  static __device__ __forceinline__ void set(uint4 &r, int i, const uint16_t *p) {
+    uint32_t &w = (&r.x)[i / 2];
+    w = i & 1 ? (w & 0xFFFFu) | ((uint32_t)__ldg(p) << 16) : (w & 0xFFFF0000u) | __ldg(p);
+  }
+  static __device__ __forceinline__ void open(const uint4 &r, float f[8]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       f[2 * t] = __uint_as_float(w[t] << 16);
       f[2 * t + 1] = __uint_as_float(w[t] & 0xFFFF0000u);
     }
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float largest(const uint4 &r) {
+    const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
 };
 
@@ -92,15 +112,30 @@ struct Stats {
 
 // Joins two triples (order matters only in the last bits).
 __device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
-  const float m = max_nan(a.m, b.m);
+  const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return a;
-  const float da = a.m - m, db = b.m - m;  // one of them 0; -inf where a side is empty
+  const float da = fmaxf((a.m - m) * kLog2E, -kLowest), db = fmaxf((b.m - m) * kLog2E, -kLowest);  // one of them 0
   const float fa = tc::ex2(da), fb = tc::ex2(db);
   Stats r;
   r.m = m;
   r.s = a.s * fa + b.s * fb;
   r.u = (fa > 0.f ? fa * (a.u + da * a.s) : 0.f) + (fb > 0.f ? fb * (b.u + db * b.s) : 0.f);
   return r;
+}
+
+// (d0, d1) = ((a0, a1) + b) * c, each operation rounded.
+__device__ __forceinline__ void add_scale2(float a0, float a1, float b, float c, float &d0, float &d1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmul.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+// (u0, u1) += (a0, a1) * (b0, b1)
+__device__ __forceinline__ void fma2(float &u0, float &u1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 u, a, b;\n\t"
+      "mov.b64 u, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "fma.rn.f32x2 u, a, b, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(u0), "+f"(u1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 // Descending bitonic sort of one key per lane.
@@ -155,236 +190,334 @@ struct RowView {
     vectors = (n + skew + Row<T>::kVec - 1) / Row<T>::kVec;
   }
   __device__ __forceinline__ int first(int j) const { return j * Row<T>::kVec - skew; }
-  __device__ __forceinline__ bool whole(int j) const {
-    return first(j) >= 0 && first(j) + Row<T>::kVec <= vocab;
+  __device__ __forceinline__ uint4 read_whole(int j) const {
+    return __ldg(reinterpret_cast<const uint4 *>(p + first(j)));
   }
-  // Elements of vector j; those outside the row read as -inf.
-  __device__ __forceinline__ void read(int j, float f[Row<T>::kVec]) const {
+  // Vector j; elements outside the row read as -inf.
+  __device__ __forceinline__ uint4 read(int j) const {
     const int e = first(j);
-    if (whole(j)) {
-      Row<T>::vec(p + e, f);
-    } else {
+    if (e >= 0 && e + Row<T>::kVec <= vocab) return read_whole(j);
+    uint4 r = make_uint4(Row<T>::kNone, Row<T>::kNone, Row<T>::kNone, Row<T>::kNone);
 #pragma unroll
-      for (int i = 0; i < Row<T>::kVec; ++i)
-        f[i] = e + i >= 0 && e + i < vocab ? Row<T>::one(p + e + i) : -INFINITY;
-    }
+    for (int i = 0; i < Row<T>::kVec; ++i)
+      if (e + i >= 0 && e + i < vocab) Row<T>::set(r, i, p + e + i);
+    return r;
   }
 };
 
-// The sums of a row whose largest logit `top` is kHuge or more in magnitude and finite: differences first,
-// so that nothing overflows (rare; every thread over its own vectors, then joined as usual).
-template <typename T, int THREADS>
-__device__ __noinline__ Stats row_stats_huge(const RowView<T> &row, float top) {
-  constexpr int V = Row<T>::kVec;
-  Stats st{0.f, 0.f, 0.f};
-  for (int j = threadIdx.x; j < row.vectors; j += THREADS) {
-    float f[V];
-    row.read(j, f);
+// What one thread has seen.
+template <typename T>
+struct Scan {
+  static constexpr int V = Row<T>::kVec;
+  float top = -INFINITY;  // its largest logit (NaN once it has seen one)
+  int top_vec;            // the first vector that holds it
+  float m = -INFINITY, s[4] = {}, u[4] = {};
+
+  template <int U>
+  __device__ __forceinline__ void take(const uint4 (&r)[U], int j, int step) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float t = (f[i] - top) * kLog2E, p = tc::ex2(t);
-      if (p > 0.f) {
-        st.s += p;
-        st.u = fmaf(p, t, st.u);
+    for (int g = 0; g < U; ++g) {
+      const float v = Row<T>::largest(r[g]);
+      if (v > top || (v != v && top == top)) {
+        top = v;
+        top_vec = j + g * step;
+      }
+    }
+    if (!(top > -INFINITY)) return;
+    if (top > m) {
+      if (m != -INFINITY) {
+        const float d = fmaxf((m - top) * kLog2E, -kLowest), e = tc::ex2(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u[i] = e * fmaf(d, s[i], u[i]);
+          s[i] *= e;
+        }
+      }
+      m = top;
+    }
+#pragma unroll
+    for (int g = 0; g < U; ++g) {
+      float f[V];
+      Row<T>::open(r[g], f);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        float t0, t1;
+        add_scale2(f[i], f[i + 1], -m, kLog2E, t0, t1);
+        t0 = fmaxf(t0, -kLowest);
+        t1 = fmaxf(t1, -kLowest);
+        const float p0 = tc::ex2(t0), p1 = tc::ex2(t1);
+        constexpr int kPairs = 2;
+        const int h = (i / 2) % kPairs * 2;
+        tc::add2(s[h], s[h + 1], p0, p1);
+        fma2(u[h], u[h + 1], p0, p1, t0, t1);
       }
     }
   }
-  return st;
+  __device__ __forceinline__ Stats stats() const {
+    return {m, (s[0] + s[1]) + (s[2] + s[3]), (u[0] + u[1]) + (u[2] + u[3])};
+  }
+};
+
+// Shared memory of a block; `row_*` are of use in a row's first block.
+template <int THREADS>
+struct Shared {
+  static constexpr int WARPS = THREADS / 32;
+  // logits that may reach the bound before the slow selection: 8 of every thread at most
+  static constexpr int kCandidates = THREADS < 128 ? 8 * THREADS : 1024;
+  Stats warp_stats[WARPS];
+  float warp_top[WARPS];
+  uint64_t list[WARPS][32];
+  uint64_t cand[kCandidates];
+  uint64_t bound;
+  int hot[THREADS];
+  int n_hot, n_cand;
+  Stats row_stats[kMaxSplits];
+  float row_top[kMaxSplits];
+  uint64_t row_list[kMaxSplits][32];
+};
+
+template <typename V>
+__device__ __forceinline__ void put_first(V *p, const V &v) {  // p's counterpart in the cluster's block 0
+  static_assert(sizeof(V) % 4 == 0, "words");
+  const uint32_t at = tc::map_to_rank(p, 0);
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i) tc::st_remote_u32(at + 4 * i, w[i]);
 }
 
+// THREADS threads a block, `splits` blocks (a cluster, if more than one) a row.
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 logprobs_kernel(const LogprobArgs a) {
   constexpr int V = Row<T>::kVec, WARPS = THREADS / 32, U = 4;
-  __shared__ Stats warp_stats[WARPS];
-  __shared__ uint64_t list[WARPS][32];
-  __shared__ uint64_t cand[kCandidates];
-  __shared__ uint64_t s_bound;
-  __shared__ int hot[THREADS];
-  __shared__ int n_hot, n_cand;
-  __shared__ float s_top;
-  __shared__ double s_lse2;  // log2 of the sum of 2^(x log2 e)
+  using Sh = Shared<THREADS>;
+  __shared__ Sh sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t r = blockIdx.x;
+  const int part = a.splits > 1 ? (int)(blockIdx.x % (unsigned)a.splits) : 0;
+  const int64_t r = a.splits > 1 ? blockIdx.x / (unsigned)a.splits : blockIdx.x;
   const RowView<T> row(static_cast<const T *>(a.logits) + r * a.ld, a.vocab);
-  if (tid == 0) n_hot = n_cand = 0;
-
-  // ---- one pass: statistics, and the thread's largest logit with its vector
-  float top = -INFINITY;  // largest logit of this thread (NaN once it has seen one)
-  int top_vec = -1;
-  Stats st{-INFINITY, 0.f, 0.f};
-  auto take = [&](const float (&f)[U][V], const int (&jv)[U], int n) {
-#pragma unroll
-    for (int g = 0; g < U; ++g) {
-      if (g < n) {
-        float vm = f[g][0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) vm = max_nan(vm, f[g][i]);
-        if (top_vec < 0 || (!(vm <= top) && top == top)) {
-          top = vm;
-          top_vec = jv[g];
-        }
-      }
-    }
-    if (!(top > -kHuge)) return;
-    const float ref = top * kLog2E;
-    if (ref > st.m) {
-      if (st.m != -INFINITY) {
-        const float d = st.m - ref, e = tc::ex2(d);
-        st.u = e * (st.u + d * st.s);
-        st.s *= e;
-      }
-      st.m = ref;
-    }
-#pragma unroll
-    for (int g = 0; g < U; ++g) {
-      if (g < n) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float t = fmaf(max_nan(f[g][i], -kLowest), kLog2E, -st.m), p = tc::ex2(t);
-          st.s += p;
-          st.u = fmaf(p, t, st.u);
-        }
-      }
-    }
-  };
-  int j = tid;
-  for (; j + (U - 1) * THREADS < row.vectors; j += U * THREADS) {
-    float f[U][V];
-    int jv[U];
-#pragma unroll
-    for (int g = 0; g < U; ++g) {
-      jv[g] = j + g * THREADS;
-      row.read(jv[g], f[g]);
-    }
-    take(f, jv, U);
-  }
-  for (; j < row.vectors; j += THREADS) {
-    float f[U][V];
-    const int jv[U] = {j, 0, 0, 0};
-    row.read(j, f[0]);
-    take(f, jv, 1);
+  const int j_first = (int)((int64_t)row.vectors * part / a.splits);
+  const int j_end = (int)((int64_t)row.vectors * (part + 1) / a.splits);
+  if (tid == 0) sh.n_hot = sh.n_cand = 0;
+  if (a.splits > 1) tc::cluster_arrive();  // block 0 has to run before its memory is written
+  // the given token's logit, wanted at the end
+  int32_t target = -1;
+  float target_logit = 0.f;
+  if (tid == 0 && part == 0 && a.logprob) {
+    target = a.targets[r];
+    if (target >= 0 && target < a.vocab) target_logit = Row<T>::one(row.p + target);
   }
 
-  // ---- the row's statistics
-  float rmax = top_vec < 0 ? -INFINITY : top;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) rmax = max_nan(rmax, __shfl_xor_sync(0xFFFFFFFFu, rmax, o));
-  if (lane == 0) warp_stats[warp].m = rmax;
-  __syncthreads();
-  if (tid == 0) {
-    float m = warp_stats[0].m;
-    for (int w = 1; w < WARPS; ++w) m = max_nan(m, warp_stats[w].m);
-    s_top = m;
+  // ---- one pass: statistics, and the thread's largest logit with its vector.  The next U vectors
+  // are on their way while U are worked on.
+  Scan<T> scan;
+  int j = j_first + tid;
+  scan.top_vec = j < j_end ? j : -1;
+  // a vector that the row cuts off at its start or end is taken by itself
+  if (j == 0 && j < j_end && row.skew) {
+    const uint4 edge[1] = {row.read(0)};
+    scan.template take<1>(edge, 0, THREADS);
+    j += THREADS;
   }
-  __syncthreads();
-  const float row_top = s_top;
-  const bool huge = fabsf(row_top) >= kHuge && fabsf(row_top) < INFINITY;
-  if (huge) st = row_stats_huge<T, THREADS>(row, row_top);
+  const bool cut = j_end == row.vectors && row.first(row.vectors - 1) + V > a.vocab;
+  const int j_whole = cut ? j_end - 1 : j_end;
+  uint4 next[U];
+  if (j + (U - 1) * THREADS < j_whole) {
+#pragma unroll
+    for (int g = 0; g < U; ++g) next[g] = row.read_whole(j + g * THREADS);
+  }
+  for (; j + (U - 1) * THREADS < j_whole; j += U * THREADS) {
+    uint4 cur[U];
+#pragma unroll
+    for (int g = 0; g < U; ++g) cur[g] = next[g];
+    if (j + (2 * U - 1) * THREADS < j_whole) {
+#pragma unroll
+      for (int g = 0; g < U; ++g) next[g] = row.read_whole(j + (U + g) * THREADS);
+    }
+    scan.template take<U>(cur, j, THREADS);
+  }
+  {  // fewer than U left: their loads together, too
+    uint4 last[U];
+    const uint4 none = make_uint4(Row<T>::kNone, Row<T>::kNone, Row<T>::kNone, Row<T>::kNone);
+#pragma unroll
+    for (int g = 0; g < U; ++g) {
+      const int jj = j + g * THREADS;
+      last[g] = none;
+      if (jj < j_whole) last[g] = row.read_whole(jj);
+      else if (jj < j_end) last[g] = row.read(jj);
+    }
+    if (j < j_end) scan.template take<U>(last, j, THREADS);
+  }
+
+  // ---- the statistics of the block's part
+  float top = scan.top;
+  Stats st = scan.stats();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Stats b;
     b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
     b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
     b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
+    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     st = lane & o ? join(b, st) : join(st, b);
   }
-  if (lane == 0) warp_stats[warp] = st;
-  __syncthreads();
-  if (tid == 0) {
-    Stats t = warp_stats[0];
-    for (int w = 1; w < WARPS; ++w) t = join(t, warp_stats[w]);
-    // the distribution's logarithm, relative to the row's largest logit where that is huge
-    const bool none = !(row_top > -INFINITY) || row_top == INFINITY;
-    const double nan = __longlong_as_double(0x7FF8000000000000ll);
-    const double lse2 = none ? nan : (double)t.m + log2((double)t.s);
-    s_lse2 = lse2;
-    if (a.entropy) a.entropy[r] = none ? (float)nan : (float)(kLn2 * (log2((double)t.s) - (double)t.u / (double)t.s));
-    if (a.logprob) {
-      const int32_t g = a.targets[r];
-      float v = (float)nan;
-      if (g == -1) v = 0.f;
-      else if (g >= 0 && g < a.vocab) {
-        const float x = Row<T>::one(row.p + g);
-        v = huge ? (float)((double)x - (double)row_top - kLn2 * lse2)
-                 : (float)(kLn2 * ((double)x * (double)kLog2E - lse2));
+  if (lane == 0) {
+    sh.warp_stats[warp] = st;
+    sh.warp_top[warp] = top;
+  }
+
+  // ---- alternatives of the block's part: the bound, the logits that reach it, the largest in order
+  uint64_t k = 0;
+  if (a.top != 0) {
+    const uint64_t mine = scan.top_vec < 0 ? 0 : key_of(order_of(scan.top), (uint32_t)scan.top_vec);
+    k = block_merge<WARPS>(warp_sort(mine), sh.list);
+    if (warp == 0 && lane == a.top - 1) sh.bound = k;
+    __syncthreads();
+    const uint64_t bound = sh.bound;  // 0: fewer threads than that have any logit
+    if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = tid;
+    __syncthreads();
+    for (int i = warp; i < sh.n_hot; i += WARPS) {
+      for (int jj = j_first + sh.hot[i] + lane * THREADS; jj < j_end; jj += 32 * THREADS) {
+        float f[V];
+        Row<T>::open(row.read(jj), f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t o = order_of(f[e]);
+          const int index = row.first(jj) + e;
+          if (key_of(o, (uint32_t)jj) >= bound && index >= 0 && index < a.vocab) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < Sh::kCandidates) sh.cand[at] = key_of(o, (uint32_t)index);
+          }
+        }
       }
+    }
+    __syncthreads();
+    if (sh.n_cand <= Sh::kCandidates) {
+      k = 0;
+      for (int i = warp * 32; i < sh.n_cand; i += THREADS) {
+        const uint64_t c = warp_sort(i + lane < sh.n_cand ? sh.cand[i + lane] : 0);
+        k = warp_merge(k, c);
+      }
+      k = block_merge<WARPS>(k, sh.list);
+    } else {
+      // more than that reach the bound: take the largest key below the last one, `top` times
+      uint64_t last = ~0ull, got = 0;
+      for (int n = 0; n < a.top; ++n) {
+        uint64_t best = 0;
+        for (int jj = j_first + tid; jj < j_end; jj += THREADS) {
+          float f[V];
+          Row<T>::open(row.read(jj), f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const int index = row.first(jj) + e;
+            const uint64_t c = key_of(order_of(f[e]), (uint32_t)index);
+            if (index >= 0 && index < a.vocab && c < last && c > best) best = c;
+          }
+        }
+        best = block_merge<WARPS>(warp_sort(best), sh.list);
+        if (tid == 0) sh.bound = best;
+        __syncthreads();
+        last = sh.bound;
+        __syncthreads();
+        if (warp == 0 && lane == n) got = last;
+      }
+      k = got;
+    }
+  } else {
+    __syncthreads();  // warp_stats
+  }
+
+  // ---- the row: its parts' statistics and alternatives meet in block 0
+  if (warp == 0) {
+    st = lane < WARPS ? sh.warp_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+    top = lane < WARPS ? sh.warp_top[lane] : -INFINITY;
+#pragma unroll
+    for (int o = WARPS / 2; o > 0; o >>= 1) {
+      Stats b;
+      b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
+      b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
+      b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
+      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      st = lane & o ? join(b, st) : join(st, b);
+    }
+  }
+  if (a.splits > 1) {
+    __syncwarp();
+    tc::cluster_wait();
+    if (warp == 0) {
+      if (lane == 0) {
+        put_first(&sh.row_stats[part], st);
+        put_first(&sh.row_top[part], top);
+      }
+      if (a.top != 0) put_first(&sh.row_list[part][lane], k);
+    }
+    __syncwarp();
+    tc::cluster_sync();
+    if (part != 0 || warp != 0) return;
+    st = lane < a.splits ? sh.row_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+    top = lane < a.splits ? sh.row_top[lane] : -INFINITY;
+#pragma unroll
+    for (int o = kMaxSplits / 2; o > 0; o >>= 1) {
+      Stats b;
+      b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
+      b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
+      b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
+      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      st = lane & o ? join(b, st) : join(st, b);
+    }
+    if (a.top != 0)
+      for (int i = 1; i < a.splits; ++i) k = warp_merge(k, sh.row_list[i][lane]);
+  }
+  if (warp != 0) return;
+  top = __shfl_sync(0xFFFFFFFFu, top, 0);
+  const bool none = !(top > -INFINITY) || top == INFINITY;
+  const double nan = __longlong_as_double(0x7FF8000000000000ll);
+  const double log2s = none ? nan : log2((double)__shfl_sync(0xFFFFFFFFu, st.s, 0));
+  const double big = (double)__shfl_sync(0xFFFFFFFFu, st.m, 0);
+  if (lane == 0) {
+    if (a.entropy) a.entropy[r] = (float)(kLn2 * (log2s - (double)st.u / (double)st.s));
+    if (a.logprob) {
+      float v = (float)nan;
+      if (target == -1) v = 0.f;
+      else if (target >= 0 && target < a.vocab) v = (float)((double)target_logit - big - kLn2 * log2s);
       a.logprob[r] = v;
     }
   }
-  if (a.top == 0) return;
-
-  // ---- alternatives: the bound, the logits that reach it, the largest of them in order
-  uint64_t k = top_vec < 0 ? 0 : key_of(order_of(top), (uint32_t)top_vec);
-  const uint64_t mine = k;
-  k = block_merge<WARPS>(warp_sort(k), list);
-  if (warp == 0 && lane == a.top - 1) s_bound = k;
-  __syncthreads();
-  const uint64_t bound = s_bound;  // 0: fewer threads than that have any logit
-  if (mine != 0 && mine >= bound) hot[atomicAdd(&n_hot, 1)] = tid;
-  __syncthreads();
-  for (int i = warp; i < n_hot; i += WARPS) {
-    for (int jj = hot[i] + lane * THREADS; jj < row.vectors; jj += 32 * THREADS) {
-      float f[V];
-      row.read(jj, f);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t o = order_of(f[e]);
-        const int index = row.first(jj) + e;
-        if (key_of(o, (uint32_t)jj) >= bound && index >= 0 && index < a.vocab) {
-          const int at = atomicAdd(&n_cand, 1);
-          if (at < kCandidates) cand[at] = key_of(o, (uint32_t)index);
-        }
-      }
-    }
-  }
-  __syncthreads();
-  if (n_cand <= kCandidates) {
-    k = 0;
-    for (int i = warp * 32; i < n_cand; i += THREADS) {
-      const uint64_t c = warp_sort(i + lane < n_cand ? cand[i + lane] : 0);
-      k = warp_merge(k, c);
-    }
-    k = block_merge<WARPS>(k, list);
-  } else {
-    // more than that reach the bound: take the largest key below the last one, `top` times
-    uint64_t last = ~0ull, got = 0;
-    for (int n = 0; n < a.top; ++n) {
-      uint64_t best = 0;
-      for (int jj = tid; jj < row.vectors; jj += THREADS) {
-        float f[V];
-        row.read(jj, f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int index = row.first(jj) + e;
-          const uint64_t c = key_of(order_of(f[e]), (uint32_t)index);
-          if (index >= 0 && index < a.vocab && c < last && c > best) best = c;
-        }
-      }
-      best = block_merge<WARPS>(warp_sort(best), list);
-      if (tid == 0) s_bound = best;
-      __syncthreads();
-      last = s_bound;
-      __syncthreads();
-      if (warp == 0 && lane == n) got = last;
-    }
-    k = got;
-  }
-  if (warp == 0 && lane < a.top) {
+  if (lane < a.top) {
     const float x = value_of((uint32_t)(k >> 32));
     if (a.top_ids) a.top_ids[r * a.top + lane] = (int32_t)index_of(k);
-    if (a.top_logprobs)
-      a.top_logprobs[r * a.top + lane] =
-          huge ? (float)((double)x - (double)row_top - kLn2 * s_lse2)
-               : (float)(kLn2 * ((double)x * (double)kLog2E - s_lse2));
+    if (a.top_logprobs) a.top_logprobs[r * a.top + lane] = (float)((double)x - big - kLn2 * log2s);
   }
 }
 
+template <typename T, int THREADS>
+cudaError_t launch_one(const LogprobArgs &a, int64_t rows, cudaStream_t st) {
+  if (a.splits == 1) {
+    logprobs_kernel<T, THREADS><<<(unsigned)rows, THREADS, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * a.splits));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a);
+}
+
 template <typename T>
-cudaError_t launch(const LogprobArgs &a, int64_t rows, cudaStream_t st) {
-  if (a.vocab >= 8192) logprobs_kernel<T, 512><<<(unsigned)rows, 512, 0, st>>>(a);
-  else logprobs_kernel<T, 128><<<(unsigned)rows, 128, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch(LogprobArgs &a, int64_t rows, cudaStream_t st) {
+  const int vectors = (a.vocab + Row<T>::kVec - 1) / Row<T>::kVec;
+  a.splits = 1;
+  // several blocks a row while that leaves SMs to fill and every thread has a vector
+  while (a.splits < kMaxSplits && rows * a.splits * 2 <= 2 * kSmCount && vectors >= 2 * a.splits * 256) a.splits *= 2;
+  if (vectors >= 1024) return launch_one<T, 256>(a, rows, st);
+  if (vectors >= 256) return launch_one<T, 128>(a, rows, st);
+  return launch_one<T, 32>(a, rows, st);
 }
 
 }  // namespace
@@ -414,8 +547,8 @@ extern "C" zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int
   const DeviceScope device(ctx);
   if (device.status != cudaSuccess)
     return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
-  const LogprobArgs a{logits, ld, (int)vocab, top_ids || top_logprobs ? top : 0, targets, logprob, entropy,
-                      top_ids, top_logprobs};
+  LogprobArgs a{logits, ld, (int)vocab, top_ids || top_logprobs ? top : 0, 1, targets, logprob, entropy,
+                top_ids, top_logprobs};
   const cudaError_t e = dtype == ZO_F32 ? launch<float>(a, rows, ctx->stream)
                                         : launch<uint16_t>(a, rows, ctx->stream);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "logprobs_kernel: %s", cudaGetErrorString(e));
