@@ -28,6 +28,8 @@ constexpr double kLn2 = 0.69314718055994530942;
 // t below -kLowest (a masked logit's is -inf) counts as that: 2^t is 0 all the same, and 0 t stays 0.
 constexpr float kLowest = 1e30f;
 constexpr int kMaxSplits = 8;  // blocks of a row (a portable cluster)
+constexpr int kManyHot = 64;   // threads that reach the bound before it is made exact
+constexpr int kGroups = 16;    // groups of consecutive vectors of a thread
 
 struct LogprobArgs {
   const void *logits;
@@ -214,16 +216,18 @@ struct Scan {
   float m = -INFINITY, s[4] = {}, u[4] = {};
 
   template <int U>
-  __device__ __forceinline__ void take(const uint4 (&r)[U], int j, int step) {
+  __device__ __forceinline__ float take(const uint4 (&r)[U], int j, int step) {  // returns the largest
+    float all = -INFINITY;
 #pragma unroll
     for (int g = 0; g < U; ++g) {
       const float v = Row<T>::largest(r[g]);
+      all = max_nan(all, v);
       if (v > top || (v != v && top == top)) {
         top = v;
         top_vec = j + g * step;
       }
     }
-    if (!(top > -INFINITY)) return;
+    if (!(top > -INFINITY)) return all;
     if (top > m) {
       if (m != -INFINITY) {
         const float d = fmaxf((m - top) * kLog2E, -kLowest), e = tc::ex2(d);
@@ -252,6 +256,7 @@ struct Scan {
         fma2(u[h], u[h + 1], p0, p1, t0, t1);
       }
     }
+    return all;
   }
   __device__ __forceinline__ Stats stats() const {
     return {m, (s[0] + s[1]) + (s[2] + s[3]), (u[0] + u[1]) + (u[2] + u[3])};
@@ -269,7 +274,8 @@ struct Shared {
   uint64_t list[WARPS][32];
   uint64_t cand[kCandidates];
   uint64_t bound;
-  int hot[THREADS];
+  uint16_t group_top[kGroups][THREADS];  // order prefix of a group's largest logit
+  uint16_t hot[kManyHot * kGroups];      // threads, or thread + THREADS * group
   int n_hot, n_cand;
   Stats row_stats[kMaxSplits];
   float row_top[kMaxSplits];
@@ -309,22 +315,21 @@ logprobs_kernel(const LogprobArgs a) {
   }
 
   // ---- one pass: statistics, and the thread's largest logit with its vector.  The next U vectors
-  // are on their way while U are worked on.
+  // are on their way while U are worked on.  Only the first and the last vector of a row may be
+  // cut off by it.
   Scan<T> scan;
   int j = j_first + tid;
   scan.top_vec = j < j_end ? j : -1;
-  // a vector that the row cuts off at its start or end is taken by itself
-  if (j == 0 && j < j_end && row.skew) {
-    const uint4 edge[1] = {row.read(0)};
-    scan.template take<1>(edge, 0, THREADS);
-    j += THREADS;
-  }
   const bool cut = j_end == row.vectors && row.first(row.vectors - 1) + V > a.vocab;
   const int j_whole = cut ? j_end - 1 : j_end;
+  const int group_rounds = ((j_end - j_first - 1) / (U * THREADS) + kGroups) / kGroups;  // rounds of U a group
+  int round = 0, group = 0;
+  float group_top = -INFINITY;
   uint4 next[U];
   if (j + (U - 1) * THREADS < j_whole) {
+    next[0] = row.read(j);
 #pragma unroll
-    for (int g = 0; g < U; ++g) next[g] = row.read_whole(j + g * THREADS);
+    for (int g = 1; g < U; ++g) next[g] = row.read_whole(j + g * THREADS);
   }
   for (; j + (U - 1) * THREADS < j_whole; j += U * THREADS) {
     uint4 cur[U];
@@ -334,20 +339,24 @@ logprobs_kernel(const LogprobArgs a) {
 #pragma unroll
       for (int g = 0; g < U; ++g) next[g] = row.read_whole(j + (U + g) * THREADS);
     }
-    scan.template take<U>(cur, j, THREADS);
+    group_top = max_nan(group_top, scan.template take<U>(cur, j, THREADS));
+    if (++round == group_rounds) {
+      sh.group_top[group++][tid] = (uint16_t)(order_of(group_top) >> 16);
+      group_top = -INFINITY;
+      round = 0;
+    }
   }
-  {  // fewer than U left: their loads together, too
+  if (j < j_end) {  // fewer than U left: their loads together, too
     uint4 last[U];
-    const uint4 none = make_uint4(Row<T>::kNone, Row<T>::kNone, Row<T>::kNone, Row<T>::kNone);
 #pragma unroll
     for (int g = 0; g < U; ++g) {
-      const int jj = j + g * THREADS;
-      last[g] = none;
-      if (jj < j_whole) last[g] = row.read_whole(jj);
-      else if (jj < j_end) last[g] = row.read(jj);
+      last[g] = make_uint4(Row<T>::kNone, Row<T>::kNone, Row<T>::kNone, Row<T>::kNone);
+      if (j + g * THREADS < j_end) last[g] = row.read(j + g * THREADS);
     }
-    if (j < j_end) scan.template take<U>(last, j, THREADS);
+    group_top = max_nan(group_top, scan.template take<U>(last, j, THREADS));
+    ++round;
   }
+  if (round) sh.group_top[group++][tid] = (uint16_t)(order_of(group_top) >> 16);
 
   // ---- the statistics of the block's part
   float top = scan.top;
@@ -366,62 +375,95 @@ logprobs_kernel(const LogprobArgs a) {
     sh.warp_top[warp] = top;
   }
 
-  // ---- alternatives of the block's part: the bound, the logits that reach it, the largest in order
+  // ---- alternatives of the block's part: the bound, then the logits that reach it
   uint64_t k = 0;
   if (a.top != 0) {
     const uint64_t mine = scan.top_vec < 0 ? 0 : key_of(order_of(scan.top), (uint32_t)scan.top_vec);
-    k = block_merge<WARPS>(warp_sort(mine), sh.list);
-    if (warp == 0 && lane == a.top - 1) sh.bound = k;
-    __syncthreads();
-    const uint64_t bound = sh.bound;  // 0: fewer threads than that have any logit
-    if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = tid;
-    __syncthreads();
-    for (int i = warp; i < sh.n_hot; i += WARPS) {
-      for (int jj = j_first + sh.hot[i] + lane * THREADS; jj < j_end; jj += 32 * THREADS) {
-        float f[V];
-        Row<T>::open(row.read(jj), f);
+    // the largest 16-bit prefix of an order that the keys of `top` threads reach, if that many have one
+    uint32_t prefix = 0;
+    int reach = THREADS;
+#pragma unroll 1
+    for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1) {
+      const int n = __syncthreads_count((uint32_t)(mine >> 48) >= (prefix | bit));
+      if (n >= a.top) {
+        prefix |= bit;
+        reach = n;
+      }
+    }
+    uint64_t bound = (uint64_t)prefix << 48;
+    if (reach > kManyHot) {  // many alike: the exact key
+      k = block_merge<WARPS>(warp_sort(mine), sh.list);
+      if (warp == 0 && lane == a.top - 1) sh.bound = k;
+      __syncthreads();
+      bound = sh.bound;  // 0: fewer threads than that have any logit
+    }
+    // vector jj again: its logits that reach the bound
+    auto gather = [&](int jj) {
+      float f[V];
+      Row<T>::open(row.read(jj), f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const uint32_t o = order_of(f[e]);
-          const int index = row.first(jj) + e;
-          if (key_of(o, (uint32_t)jj) >= bound && index >= 0 && index < a.vocab) {
-            const int at = atomicAdd(&sh.n_cand, 1);
-            if (at < Sh::kCandidates) sh.cand[at] = key_of(o, (uint32_t)index);
-          }
+      for (int e = 0; e < V; ++e) {
+        const uint32_t o = order_of(f[e]);
+        const int index = row.first(jj) + e;
+        if (key_of(o, (uint32_t)jj) >= bound && index >= 0 && index < a.vocab) {
+          const int at = atomicAdd(&sh.n_cand, 1);
+          if (at < Sh::kCandidates) sh.cand[at] = key_of(o, (uint32_t)index);
         }
+      }
+    };
+    if (reach > kManyHot) {
+      if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)tid;
+      __syncthreads();
+      for (int i = warp; i < sh.n_hot; i += WARPS)
+        for (int jj = j_first + sh.hot[i] + lane * THREADS; jj < j_end; jj += 32 * THREADS) gather(jj);
+    } else {
+      if (mine != 0 && mine >= bound)
+        for (int g = 0; g < group; ++g)
+          if (sh.group_top[g][tid] >= prefix) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)(tid + THREADS * g);
+      __syncthreads();
+      const int per = U * group_rounds;  // vectors of a group
+      for (int i = tid; i < sh.n_hot * per; i += THREADS) {
+        const int h = sh.hot[i / per];
+        const int jj = j_first + h % THREADS + (h / THREADS * per + i % per) * THREADS;
+        if (jj < j_end) gather(jj);
       }
     }
     __syncthreads();
-    if (sh.n_cand <= Sh::kCandidates) {
-      k = 0;
-      for (int i = warp * 32; i < sh.n_cand; i += THREADS) {
-        const uint64_t c = warp_sort(i + lane < sh.n_cand ? sh.cand[i + lane] : 0);
-        k = warp_merge(k, c);
-      }
-      k = block_merge<WARPS>(k, sh.list);
-    } else {
-      // more than that reach the bound: take the largest key below the last one, `top` times
-      uint64_t last = ~0ull, got = 0;
-      for (int n = 0; n < a.top; ++n) {
-        uint64_t best = 0;
-        for (int jj = j_first + tid; jj < j_end; jj += THREADS) {
-          float f[V];
-          Row<T>::open(row.read(jj), f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const int index = row.first(jj) + e;
-            const uint64_t c = key_of(order_of(f[e]), (uint32_t)index);
-            if (index >= 0 && index < a.vocab && c < last && c > best) best = c;
-          }
+    const int n_list = sh.n_cand;
+    if (n_list > 32) {
+      if (n_list <= Sh::kCandidates) {
+        k = 0;
+        for (int i = warp * 32; i < n_list; i += THREADS) {
+          const uint64_t c = warp_sort(i + lane < n_list ? sh.cand[i + lane] : 0);
+          k = warp_merge(k, c);
         }
-        best = block_merge<WARPS>(warp_sort(best), sh.list);
-        if (tid == 0) sh.bound = best;
-        __syncthreads();
-        last = sh.bound;
-        __syncthreads();
-        if (warp == 0 && lane == n) got = last;
+        k = block_merge<WARPS>(k, sh.list);
+      } else {
+        // more than that reach the bound: take the largest key below the last one, `top` times
+        uint64_t last = ~0ull, got = 0;
+        for (int n = 0; n < a.top; ++n) {
+          uint64_t best = 0;
+          for (int jj = j_first + tid; jj < j_end; jj += THREADS) {
+            float f[V];
+            Row<T>::open(row.read(jj), f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const int index = row.first(jj) + e;
+              const uint64_t c = key_of(order_of(f[e]), (uint32_t)index);
+              if (index >= 0 && index < a.vocab && c < last && c > best) best = c;
+            }
+          }
+          best = block_merge<WARPS>(warp_sort(best), sh.list);
+          if (tid == 0) sh.bound = best;
+          __syncthreads();
+          last = sh.bound;
+          __syncthreads();
+          if (warp == 0 && lane == n) got = last;
+        }
+        k = got;
       }
-      k = got;
+    } else if (warp == 0) {
+      k = lane < n_list ? sh.cand[lane] : 0;
     }
   } else {
     __syncthreads();  // warp_stats
@@ -453,7 +495,17 @@ logprobs_kernel(const LogprobArgs a) {
     }
     __syncwarp();
     tc::cluster_sync();
-    if (part != 0 || warp != 0) return;
+    if (part != 0) return;
+    if (a.top != 0) {
+      if (WARPS >= kMaxSplits) {
+        k = warp_sort(warp < a.splits ? sh.row_list[warp][lane] : 0);
+        k = block_merge<WARPS>(k, sh.list);
+      } else if (warp == 0) {
+        k = 0;
+        for (int i = 0; i < a.splits; ++i) k = warp_merge(k, warp_sort(sh.row_list[i][lane]));
+      }
+    }
+    if (warp != 0) return;
     st = lane < a.splits ? sh.row_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
     top = lane < a.splits ? sh.row_top[lane] : -INFINITY;
 #pragma unroll
@@ -465,10 +517,10 @@ logprobs_kernel(const LogprobArgs a) {
       top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       st = lane & o ? join(b, st) : join(st, b);
     }
-    if (a.top != 0)
-      for (int i = 1; i < a.splits; ++i) k = warp_merge(k, sh.row_list[i][lane]);
+  } else {
+    if (warp != 0) return;
+    if (a.top != 0 && sh.n_cand <= 32) k = warp_sort(k);
   }
-  if (warp != 0) return;
   top = __shfl_sync(0xFFFFFFFFu, top, 0);
   const bool none = !(top > -INFINITY) || top == INFINITY;
   const double nan = __longlong_as_double(0x7FF8000000000000ll);
@@ -514,9 +566,10 @@ cudaError_t launch(LogprobArgs &a, int64_t rows, cudaStream_t st) {
   const int vectors = (a.vocab + Row<T>::kVec - 1) / Row<T>::kVec;
   a.splits = 1;
   // several blocks a row while that leaves SMs to fill and every thread has a vector
-  while (a.splits < kMaxSplits && rows * a.splits * 2 <= 2 * kSmCount && vectors >= 2 * a.splits * 256) a.splits *= 2;
-  if (vectors >= 1024) return launch_one<T, 256>(a, rows, st);
-  if (vectors >= 256) return launch_one<T, 128>(a, rows, st);
+  while (a.splits < kMaxSplits && rows * a.splits <= kSmCount && vectors >= 2 * a.splits * 256) a.splits *= 2;
+  // Few threads hold more logits each above the bound than it has to let through.
+  if (vectors >= 1024 || a.top > 16) return launch_one<T, 256>(a, rows, st);
+  if (vectors >= 256 || a.top > 4) return launch_one<T, 128>(a, rows, st);
   return launch_one<T, 32>(a, rows, st);
 }
 
