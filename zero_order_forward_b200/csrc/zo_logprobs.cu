@@ -31,9 +31,12 @@ constexpr int kMaxSplits = 8;  // blocks of a row (a portable cluster)
 constexpr int kManyHot = 64;   // threads that reach the bound before it is made exact
 constexpr int kGroups = 16;    // groups of consecutive vectors of a thread
 
+// Rows of a block: a warp's rows need no barrier of the block, and blocks of one warp start too slowly.
+__host__ __device__ constexpr int rows_of_block(int threads) { return threads == 32 ? 4 : 1; }
+
 struct LogprobArgs {
   const void *logits;
-  int64_t ld;
+  int64_t ld, rows;
   int vocab, top, splits;
   const int32_t *targets;
   float *logprob, *entropy;
@@ -112,17 +115,24 @@ struct Stats {
   float m, s, u;  // see above; m = -inf: nothing yet (s = u = 0)
 };
 
-// Joins two triples (order matters only in the last bits).
-__device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return a;
-  const float da = fmaxf((a.m - m) * kLog2E, -kLowest), db = fmaxf((b.m - m) * kLog2E, -kLowest);  // one of them 0
-  const float fa = tc::ex2(da), fb = tc::ex2(db);
-  Stats r;
-  r.m = m;
-  r.s = a.s * fa + b.s * fb;
-  r.u = (fa > 0.f ? fa * (a.u + da * a.s) : 0.f) + (fb > 0.f ? fb * (b.u + db * b.s) : 0.f);
-  return r;
+// The lanes' triples joined, in every lane: the sums relative to the largest m, then added in a
+// tree of fixed order.  top: the largest of the lanes', NaN if one is.
+__device__ __forceinline__ void warp_join(Stats &t, float &top) {
+  float m = t.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  }
+  const float d = fmaxf((t.m - m) * kLog2E, -kLowest), f = tc::ex2(d);  // (-inf) - (-inf): -kLowest
+  t.u = f > 0.f ? f * fmaf(d, t.s, t.u) : 0.f;
+  t.s *= f;
+  t.m = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
+    t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, o);
+  }
 }
 
 // (d0, d1) = ((a0, a1) + b) * c, each operation rounded.
@@ -165,6 +175,17 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
     k = (k > o) == ((lane & stride) == 0) ? k : o;
   }
   return k;
+}
+
+// Barrier over a row's threads, and the count of those whose `p` holds.
+template <int THREADS>
+__device__ __forceinline__ void row_sync() {
+  if (THREADS == 32) __syncwarp();
+  else __syncthreads();
+}
+template <int THREADS>
+__device__ __forceinline__ int row_count(bool p) {
+  return THREADS == 32 ? __popc(__ballot_sync(0xFFFFFFFFu, p)) : __syncthreads_count(p);
 }
 
 // The 32 largest of all warps' sorted lists, in lanes of warp 0 (descending).  All threads call.
@@ -293,14 +314,17 @@ __device__ __forceinline__ void put_first(V *p, const V &v) {  // p's counterpar
 
 // THREADS threads a block, `splits` blocks (a cluster, if more than one) a row.
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+__global__ void __launch_bounds__(THREADS * rows_of_block(THREADS), 1024 / (THREADS * rows_of_block(THREADS)))
 logprobs_kernel(const LogprobArgs a) {
   constexpr int V = Row<T>::kVec, WARPS = THREADS / 32, U = 4;
   using Sh = Shared<THREADS>;
-  __shared__ Sh sh;
+  __shared__ Sh shared[rows_of_block(THREADS)];
+  Sh &sh = shared[threadIdx.y];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = a.splits > 1 ? (int)(blockIdx.x % (unsigned)a.splits) : 0;
-  const int64_t r = a.splits > 1 ? blockIdx.x / (unsigned)a.splits : blockIdx.x;
+  const int64_t r = rows_of_block(THREADS) * (int64_t)(a.splits > 1 ? blockIdx.x / (unsigned)a.splits : blockIdx.x) +
+                    threadIdx.y;
+  if (rows_of_block(THREADS) > 1 && r >= a.rows) return;
   const RowView<T> row(static_cast<const T *>(a.logits) + r * a.ld, a.vocab);
   const int j_first = (int)((int64_t)row.vectors * part / a.splits);
   const int j_end = (int)((int64_t)row.vectors * (part + 1) / a.splits);
@@ -346,14 +370,18 @@ logprobs_kernel(const LogprobArgs a) {
       round = 0;
     }
   }
-  if (j < j_end) {  // fewer than U left: their loads together, too
+  if (j < j_end) {  // at most U left: their loads together, too
     uint4 last[U];
 #pragma unroll
-    for (int g = 0; g < U; ++g) {
-      last[g] = make_uint4(Row<T>::kNone, Row<T>::kNone, Row<T>::kNone, Row<T>::kNone);
+    for (int g = 0; g < U; ++g)
       if (j + g * THREADS < j_end) last[g] = row.read(j + g * THREADS);
+#pragma unroll
+    for (int g = 0; g < U; ++g) {
+      if (j + g * THREADS < j_end) {
+        const uint4 one[1] = {last[g]};
+        group_top = max_nan(group_top, scan.template take<1>(one, j + g * THREADS, THREADS));
+      }
     }
-    group_top = max_nan(group_top, scan.template take<U>(last, j, THREADS));
     ++round;
   }
   if (round) sh.group_top[group++][tid] = (uint16_t)(order_of(group_top) >> 16);
@@ -361,15 +389,7 @@ logprobs_kernel(const LogprobArgs a) {
   // ---- the statistics of the block's part
   float top = scan.top;
   Stats st = scan.stats();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stats b;
-    b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-    b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
-    b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
-    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    st = lane & o ? join(b, st) : join(st, b);
-  }
+  warp_join(st, top);
   if (lane == 0) {
     sh.warp_stats[warp] = st;
     sh.warp_top[warp] = top;
@@ -384,7 +404,7 @@ logprobs_kernel(const LogprobArgs a) {
     int reach = THREADS;
 #pragma unroll 1
     for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1) {
-      const int n = __syncthreads_count((uint32_t)(mine >> 48) >= (prefix | bit));
+      const int n = row_count<THREADS>((uint32_t)(mine >> 48) >= (prefix | bit));
       if (n >= a.top) {
         prefix |= bit;
         reach = n;
@@ -394,7 +414,7 @@ logprobs_kernel(const LogprobArgs a) {
     if (reach > kManyHot) {  // many alike: the exact key
       k = block_merge<WARPS>(warp_sort(mine), sh.list);
       if (warp == 0 && lane == a.top - 1) sh.bound = k;
-      __syncthreads();
+      row_sync<THREADS>();
       bound = sh.bound;  // 0: fewer threads than that have any logit
     }
     // vector jj again: its logits that reach the bound
@@ -413,14 +433,14 @@ logprobs_kernel(const LogprobArgs a) {
     };
     if (reach > kManyHot) {
       if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)tid;
-      __syncthreads();
+      row_sync<THREADS>();
       for (int i = warp; i < sh.n_hot; i += WARPS)
         for (int jj = j_first + sh.hot[i] + lane * THREADS; jj < j_end; jj += 32 * THREADS) gather(jj);
     } else {
       if (mine != 0 && mine >= bound)
         for (int g = 0; g < group; ++g)
           if (sh.group_top[g][tid] >= prefix) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)(tid + THREADS * g);
-      __syncthreads();
+      row_sync<THREADS>();
       const int per = U * group_rounds;  // vectors of a group
       for (int i = tid; i < sh.n_hot * per; i += THREADS) {
         const int h = sh.hot[i / per];
@@ -428,7 +448,7 @@ logprobs_kernel(const LogprobArgs a) {
         if (jj < j_end) gather(jj);
       }
     }
-    __syncthreads();
+    row_sync<THREADS>();
     const int n_list = sh.n_cand;
     if (n_list > 32) {
       if (n_list <= Sh::kCandidates) {
@@ -455,9 +475,9 @@ logprobs_kernel(const LogprobArgs a) {
           }
           best = block_merge<WARPS>(warp_sort(best), sh.list);
           if (tid == 0) sh.bound = best;
-          __syncthreads();
+          row_sync<THREADS>();
           last = sh.bound;
-          __syncthreads();
+          row_sync<THREADS>();
           if (warp == 0 && lane == n) got = last;
         }
         k = got;
@@ -466,21 +486,15 @@ logprobs_kernel(const LogprobArgs a) {
       k = lane < n_list ? sh.cand[lane] : 0;
     }
   } else {
-    __syncthreads();  // warp_stats
+    row_sync<THREADS>();  // warp_stats
   }
 
   // ---- the row: its parts' statistics and alternatives meet in block 0
   if (warp == 0) {
-    st = lane < WARPS ? sh.warp_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
-    top = lane < WARPS ? sh.warp_top[lane] : -INFINITY;
-#pragma unroll
-    for (int o = WARPS / 2; o > 0; o >>= 1) {
-      Stats b;
-      b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-      b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
-      b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
-      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      st = lane & o ? join(b, st) : join(st, b);
+    if (WARPS > 1) {
+      st = lane < WARPS ? sh.warp_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+      top = lane < WARPS ? sh.warp_top[lane] : -INFINITY;
+      warp_join(st, top);
     }
   }
   if (a.splits > 1) {
@@ -508,15 +522,7 @@ logprobs_kernel(const LogprobArgs a) {
     if (warp != 0) return;
     st = lane < a.splits ? sh.row_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
     top = lane < a.splits ? sh.row_top[lane] : -INFINITY;
-#pragma unroll
-    for (int o = kMaxSplits / 2; o > 0; o >>= 1) {
-      Stats b;
-      b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-      b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
-      b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
-      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      st = lane & o ? join(b, st) : join(st, b);
-    }
+    warp_join(st, top);
   } else {
     if (warp != 0) return;
     if (a.top != 0 && sh.n_cand <= 32) k = warp_sort(k);
@@ -545,7 +551,8 @@ logprobs_kernel(const LogprobArgs a) {
 template <typename T, int THREADS>
 cudaError_t launch_one(const LogprobArgs &a, int64_t rows, cudaStream_t st) {
   if (a.splits == 1) {
-    logprobs_kernel<T, THREADS><<<(unsigned)rows, THREADS, 0, st>>>(a);
+    constexpr int kRows = rows_of_block(THREADS);
+    logprobs_kernel<T, THREADS><<<(unsigned)((rows + kRows - 1) / kRows), dim3(THREADS, kRows), 0, st>>>(a);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
@@ -568,8 +575,8 @@ cudaError_t launch(LogprobArgs &a, int64_t rows, cudaStream_t st) {
   // several blocks a row while that leaves SMs to fill and every thread has a vector
   while (a.splits < kMaxSplits && rows * a.splits <= kSmCount && vectors >= 2 * a.splits * 256) a.splits *= 2;
   // Few threads hold more logits each above the bound than it has to let through.
-  if (vectors >= 1024 || a.top > 16) return launch_one<T, 256>(a, rows, st);
-  if (vectors >= 256 || a.top > 4) return launch_one<T, 128>(a, rows, st);
+  if (vectors >= 1024) return launch_one<T, 256>(a, rows, st);
+  if (vectors >= 256 || a.top > 8) return launch_one<T, 128>(a, rows, st);
   return launch_one<T, 32>(a, rows, st);
 }
 
@@ -600,7 +607,7 @@ extern "C" zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int
   const DeviceScope device(ctx);
   if (device.status != cudaSuccess)
     return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
-  LogprobArgs a{logits, ld, (int)vocab, top_ids || top_logprobs ? top : 0, 1, targets, logprob, entropy,
+  LogprobArgs a{logits, ld, rows, (int)vocab, top_ids || top_logprobs ? top : 0, 1, targets, logprob, entropy,
                 top_ids, top_logprobs};
   const cudaError_t e = dtype == ZO_F32 ? launch<float>(a, rows, ctx->stream)
                                         : launch<uint16_t>(a, rows, ctx->stream);
