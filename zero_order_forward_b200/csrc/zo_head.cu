@@ -10,9 +10,11 @@
 // they see, and write one triple per row at the end.  A second kernel joins a row's triples in a
 // fixed order.
 //
-// One CTA takes 128 rows and a contiguous range of W's rows in units of 32 (so that the ranges of
-// 148 CTAs differ by one unit, not by one 256-row tile), 256 at a time; the last tile of a range
-// may be narrower (the MMA's N and the number of loaded boxes follow).
+// Up to 128 rows, one CTA of every SM takes them all and a contiguous range of W's rows in units
+// of 32 (so that ranges differ by one unit, not by one tile), 256 at a time; the last tile of a
+// range may be narrower (the MMA's N and the number of loaded boxes follow).  More rows run on CTA
+// pairs (cta_group::2): 256 rows, each CTA holding 128 of them and half of W's tile, which takes two
+// thirds of the shared-memory traffic; ranges in units of 64.
 #include <cmath>
 
 #include "zo_internal.cuh"
@@ -23,15 +25,19 @@ namespace {
 
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
-constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
-constexpr int kUnit = 32;  // rows of W in one TMA box, and the unit of a CTA's range
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kBox = 32;  // rows of W in one TMA box
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 
-struct HeadSmem {
+template <bool PAIR>
+struct HeadCfg {
+  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kUnit = PAIR ? 2 * kBox : kBox;  // unit of a range of W's rows
+  static constexpr int kRows = PAIR ? 2 * kBM : kBM;    // rows of a CTA or pair
   static constexpr uint32_t kABytes = kBM * kBK * 2;
-  static constexpr uint32_t kBBytes = kBN * kBK * 2;
-  static constexpr uint32_t kBoxBytes = kUnit * kBK * 2;
+  static constexpr uint32_t kBBytes = (PAIR ? kBN / 2 : kBN) * kBK * 2;
+  static constexpr uint32_t kBoxBytes = kBox * kBK * 2;
   static constexpr uint32_t kBarOffset = kStages * (kABytes + kBBytes);
   static constexpr uint32_t kBytes = kBarOffset + 256 + 1024;
   static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barrier area");
@@ -40,7 +46,8 @@ struct HeadSmem {
 struct HeadArgs {
   int rows, vocab, width;
   int splits;             // ranges of W's rows
-  int units;              // ceil(vocab / kUnit)
+  int units;              // of W's rows
+  int a_rows;             // rows of a box of `hidden` (a multiple of 8; those behind are not loaded)
   const int32_t *targets; // may be null
   float4 *part;           // [rows][2 splits] (m, s, u, -)
   float *target_logit;    // [rows]
@@ -48,13 +55,75 @@ struct HeadArgs {
 };
 
 // Rows of W of range i: [first, last), whole units except at the end of the vocabulary.
-__host__ __device__ __forceinline__ int range_first(int i, int units, int splits) {
-  return (int)((int64_t)units * i / splits) * kUnit;
+__device__ __forceinline__ int range_first(int i, int units, int splits, int unit) {
+  return (int)((int64_t)units * i / splits) * unit;
+}
+
+// Statistics of one row over the columns that a thread sees.  m is a whole number, so that a
+// larger one rescales by an exact power of two; 32 columns are summed in fp32, in four chains,
+// their sums in fp64: one conversion and addition in 32, where fp32 sums over a vocabulary's
+// thousands of columns lose three digits more than the products do.
+struct RowStats {
+  float m = -INFINITY;
+  double s = 0.0, u = 0.0;
+
+  __device__ __forceinline__ void take(const float (&v)[32]) {
+    float x4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 4; i < 32; i += 8) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x4[c] = i + 4 < 32 ? tc::max3f(x4[c], v[i + c], v[i + 4 + c]) : fmaxf(x4[c], v[i + c]);
+    }
+    const float top = ceilf(tc::max3f(x4[0], x4[1], fmaxf(x4[2], x4[3])) * kLog2E);
+    if (top > m) {
+      if (m != -INFINITY) {
+        const float d = m - top;
+        const double e = (double)tc::ex2(d);
+        u = e * (u + (double)d * s);
+        s *= e;
+      }
+      m = top;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;  // nothing but -inf so far: 2^-inf = 0
+    float s4[4] = {}, u4[4] = {};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float t0, t1;
+      tc::fma2_bc(v[i], v[i + 1], kLog2E, -ref, t0, t1);
+      const float p0 = tc::ex2(t0), p1 = tc::ex2(t1);
+      const int h = i & 2;
+      tc::add2(s4[h], s4[h + 1], p0, p1);
+      tc::fma2(u4[h], u4[h + 1], p0, p1, t0, t1);
+    }
+    s += (double)((s4[0] + s4[1]) + (s4[2] + s4[3]));
+    u += (double)((u4[0] + u4[1]) + (u4[2] + u4[3]));
+  }
+};
+
+// The columns [c0, c0 + 32) of the tile at W's row n0 (`cols` of them exist) of one row.
+__device__ __forceinline__ void take_chunk(RowStats &st, uint32_t taddr, int n0, int c0, int cols, int target,
+                                           float *target_logit) {
+  float v[32];
+  tc::tmem_ld32(taddr + (uint32_t)c0, v);
+  const int hit = target - (n0 + c0);
+  if (__any_sync(0xFFFFFFFFu, hit >= 0 && hit < 32)) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x = i == hit ? v[i] : x;
+    if (hit >= 0 && hit < min(32, cols - c0)) *target_logit = x;
+  }
+  if (c0 + 32 > cols) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = c0 + i < cols ? v[i] : -1e30f;
+  }
+  st.take(v);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, HeadArgs a) {
-  using S = HeadSmem;
+  using S = HeadCfg<false>;
+  constexpr int kStages = S::kStages, kUnit = S::kUnit;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -69,8 +138,8 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.x * kBM, split = blockIdx.y;
-  const int n_first = range_first(split, a.units, a.splits);
-  const int n_last = min(range_first(split + 1, a.units, a.splits), a.vocab);
+  const int n_first = range_first(split, a.units, a.splits, kUnit);
+  const int n_last = min(range_first(split + 1, a.units, a.splits, kUnit), a.vocab);
   const int tiles = (n_last - n_first + kBN - 1) / kBN;
   const int nk = (a.width + kBK - 1) / kBK;
   // loaded rows of a tile: whole units (rows past the vocabulary read as zero and are masked)
@@ -108,7 +177,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
           *abort_flag = 1;
           break;
         }
-        tc::mbar_arrive_expect_tx(&full[s], S::kABytes + (uint32_t)boxes * S::kBoxBytes);
+        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)a.a_rows * kBK * 2 + (uint32_t)boxes * S::kBoxBytes);
         tc::tma_load_2d(sA + s * S::kABytes, &tmA, &full[s], kb * kBK, m0);
         for (int b = 0; b < boxes; ++b)
           tc::tma_load_2d(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, &full[s], kb * kBK,
@@ -116,6 +185,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         ++issued;
       }
     }
+    tc::pdl_launch_dependents();
   } else if (warp == 1 && lane == 0) {
     uint32_t consumed = 0;
     for (int t = 0; t < tiles && !*abort_flag; ++t) {
@@ -153,54 +223,22 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int q = warp & 3, half = (warp - 2) / 4;  // TMEM lane quadrant; half of the columns
     const int row = m0 + 32 * q + lane;
     const int target = a.targets && row < a.rows ? a.targets[row] : -1;
-    float m = -INFINITY, s = 0.f, u = 0.f;
+    const bool any = m0 + 32 * q < a.rows;  // a warp without a row only passes the accumulators on
+    RowStats st;
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
       const int b = t & 1;
-      int w = 1;
-      if (lane == 0) w = (!*abort_flag && tc::mbar_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u)) ? 1 : 0;
-      w = __shfl_sync(0xFFFFFFFFu, w, 0);
-      if (w && lane != 0) w = tc::mbar_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u) ? 1 : 0;
-      if (!__all_sync(0xFFFFFFFFu, w)) {
+      if (!tc::warp_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u, abort_flag)) {
         ok = false;
         break;
       }
       tc::tc_fence_after();
       const int n0 = n_first + t * kBN, cols = min(kBN, n_last - n0);
       const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
+      if (any) {
 #pragma unroll 1
-      for (int c0 = half * (kBN / 2); c0 < min(cols, (half + 1) * (kBN / 2)); c0 += 32) {
-        float v[32];
-        tc::tmem_ld32(base + (uint32_t)c0, v);
-        const int hit = target - (n0 + c0);
-        if (__any_sync(0xFFFFFFFFu, hit >= 0 && hit < 32)) {
-          float x = 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x = i == hit ? v[i] : x;
-          if (hit >= 0 && hit < min(32, cols - c0)) a.target_logit[row] = x;
-        }
-        if (c0 + 32 > cols) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = c0 + i < cols ? v[i] : -1e30f;
-        }
-        float mx = v[0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i) mx = fmaxf(mx, v[i]);
-        mx *= kLog2E;
-        if (mx > m) {
-          if (m != -INFINITY) {
-            const float d = m - mx, e = tc::ex2(d);
-            u = e * (u + d * s);
-            s *= e;
-          }
-          m = mx;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float x = fmaf(v[i], kLog2E, -m), p = tc::ex2(x);
-          s += p;
-          u = fmaf(p, x, u);
-        }
+        for (int c0 = half * (kBN / 2); c0 < min(cols, (half + 1) * (kBN / 2)); c0 += 32)
+          take_chunk(st, base, n0, c0, cols, target, a.target_logit + row);
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -211,7 +249,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       *abort_flag = 1;
     }
     if (row < a.rows)
-      a.part[(int64_t)row * (2 * a.splits) + 2 * split + half] = make_float4(m, s, u, 0.f);
+      a.part[(int64_t)row * (2 * a.splits) + 2 * split + half] = make_float4(st.m, (float)st.s, (float)st.u, 0.f);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -231,23 +269,187 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   }
 }
 
-// One warp per row: its triples joined lane by lane, then across the lanes.
+// The CTA-pair form: the roles of head_kernel, with the leader (CTA 0) issuing the MMAs of both and
+// each CTA's epilogue warps reading the 128 rows of its own tensor memory.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, HeadArgs a) {
+  using S = HeadCfg<true>;
+  constexpr int kStages = S::kStages, kUnit = S::kUnit;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sA = smem, *sB = smem + kStages * S::kABytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBarOffset);  // used in the leader
+  uint64_t *empty = full + kStages;
+  uint64_t *acc_full = empty + kStages;  // [2]
+  uint64_t *acc_empty = acc_full + 2;    // [2] used in the leader: both CTAs' epilogue warps
+  uint64_t *mma_done = acc_empty + 2;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+  const uint32_t rank = tc::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = (int)blockIdx.x * kBM, split = blockIdx.y;  // blockIdx.x / 2 is the pair's row tile
+  const int n_first = range_first(split, a.units, a.splits, kUnit);
+  const int n_last = min(range_first(split + 1, a.units, a.splits, kUnit), a.vocab);
+  const int tiles = (n_last - n_first + kBN - 1) / kBN;
+  const int nk = (a.width + kBK - 1) / kBK;
+  auto tile_units = [&](int t) { return min(kBN / kUnit, (n_last - n_first - t * kBN + kUnit - 1) / kUnit); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&acc_full[b], 1);
+      tc::mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    tc::mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc_pair(tmem_holder, 2 * kBN);
+  tc::tc_fence_before();
+  tc::cluster_sync();  // both CTAs' barriers initialised and tensor memory allocated
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t full_leader = tc::map_to_rank(full, 0);
+  const uint32_t acc_empty_leader = tc::map_to_rank(acc_empty, 0);
+  const uint32_t abort_peer = tc::map_to_rank(const_cast<int *>(abort_flag), rank ^ 1u);
+  auto raise_abort = [&]() {
+    atomicOr(a.err, ZO_FLAG_TIMEOUT);
+    *abort_flag = 1;
+    tc::st_remote_u32(abort_peer, 1u);
+  };
+
+  uint32_t issued = 0;
+  if (warp == 0 && lane == 0) {
+    tc::tma_prefetch_desc(&tmA);
+    tc::tma_prefetch_desc(&tmB);
+    for (int t = 0; t < tiles && !*abort_flag; ++t) {
+      const int boxes = tile_units(t);  // of each CTA: the tile's W rows split in the middle
+      const int b_row = n_first + t * kBN + (int)rank * boxes * kBox;
+      for (int kb = 0; kb < nk; ++kb) {
+        const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
+        if (*abort_flag || !tc::mbar_wait(&empty[s], ph ^ 1u)) {
+          raise_abort();
+          break;
+        }
+        if (leader) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::kABytes + (uint32_t)boxes * S::kBoxBytes));
+        tc::tma_load_2d_pair(sA + s * S::kABytes, &tmA, full_leader + 8u * s, kb * kBK, m0);
+        for (int b = 0; b < boxes; ++b)
+          tc::tma_load_2d_pair(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, full_leader + 8u * s, kb * kBK,
+                               b_row + b * kBox);
+        ++issued;
+      }
+    }
+    tc::pdl_launch_dependents();
+  } else if (warp == 1 && lane == 0 && leader) {
+    uint32_t consumed = 0;
+    for (int t = 0; t < tiles && !*abort_flag; ++t) {
+      const int b = t & 1;
+      if (!tc::mbar_wait(&acc_empty[b], ((uint32_t)(t >> 1) & 1u) ^ 1u)) {
+        raise_abort();
+        break;
+      }
+      tc::tc_fence_after();
+      const uint32_t idesc = tc::idesc_bf16_f32(2 * kBM, tile_units(t) * kUnit);
+      const uint32_t d = tmem + (uint32_t)(b * kBN);
+      for (int kb = 0; kb < nk; ++kb) {
+        const uint32_t s = consumed % kStages, ph = (consumed / kStages) & 1u;
+        if (*abort_flag || !tc::mbar_wait(&full[s], ph)) {
+          raise_abort();
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t a0 = tc::smem_addr(sA + s * S::kABytes);
+        const uint32_t b0 = tc::smem_addr(sB + s * S::kBBytes);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          tc::mma_bf16_pair(d, tc::smem_desc_k128(a0 + 32 * k), tc::smem_desc_k128(b0 + 32 * k), idesc,
+                            (kb | k) != 0 ? 1u : 0u);
+        tc::mma_commit_pair(&empty[s]);
+        ++consumed;
+      }
+      if (*abort_flag) break;
+      tc::mma_commit_pair(&acc_full[b]);
+    }
+    tc::mma_commit_pair(mma_done);  // arrives (in both CTAs) once every MMA above has retired
+  } else if (warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) / 4;
+    const int row = m0 + 32 * q + lane;
+    const int target = a.targets && row < a.rows ? a.targets[row] : -1;
+    const bool any = m0 + 32 * q < a.rows;
+    RowStats st;
+    for (int t = 0; t < tiles; ++t) {
+      const int b = t & 1;
+      if (!tc::warp_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u, abort_flag)) {
+        if (lane == 0) raise_abort();
+        break;
+      }
+      tc::tc_fence_after();
+      const int n0 = n_first + t * kBN, cols = min(kBN, n_last - n0);
+      const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
+      if (any) {
+#pragma unroll 1
+        for (int c0 = half * (kBN / 2); c0 < min(cols, (half + 1) * (kBN / 2)); c0 += 32)
+          take_chunk(st, base, n0, c0, cols, target, a.target_logit + row);
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) tc::mbar_arrive(&acc_empty[b]);
+        else tc::mbar_arrive_remote(acc_empty_leader + 8u * (uint32_t)b);
+      }
+    }
+    if (row < a.rows)
+      a.part[(int64_t)row * (2 * a.splits) + 2 * split + half] = make_float4(st.m, (float)st.s, (float)st.u, 0.f);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    if (leader) {
+      // let the pair's loads still in flight land before either CTA exits (bounded)
+      for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
+        if (issued <= s) continue;
+        const uint32_t last = s + ((issued - 1 - s) / kStages) * kStages;
+        if (!tc::mbar_wait(&full[s], (last / kStages) & 1u)) atomicOr(a.err, ZO_FLAG_TIMEOUT);
+      }
+    } else {
+      __nanosleep(1000000);  // the peer cannot observe its loads' completion: give them time
+    }
+  }
+  __syncwarp();
+  if (warp == 1) {
+    if (lane == 0 && !tc::mbar_wait(mma_done, 0)) atomicOr(a.err, ZO_FLAG_TIMEOUT);
+    __syncwarp();
+    tc::tc_fence_after();
+  }
+  tc::cluster_sync();  // no remote arrival or MMA touches either CTA after this point
+  if (warp == 1) tc::tmem_dealloc_pair(tmem, 2 * kBN);
+}
+
+// One warp per row: its triples joined lane by lane, then across the lanes, in fp64.
 __global__ void __launch_bounds__(256)
 head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  tc::pdl_wait();
   if (row >= a.rows) return;
   const float4 *part = a.part + (int64_t)row * (2 * a.splits);
   float m = -INFINITY;
   for (int i = lane; i < 2 * a.splits; i += 32) m = fmaxf(m, part[i].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float s = 0.f, u = 0.f;
+  double s = 0.0, u = 0.0;
   for (int i = lane; i < 2 * a.splits; i += 32) {
     const float4 t = part[i];
-    const float d = t.x - m, e = tc::ex2(d);
-    if (t.x != -INFINITY) {  // a half tile that held no column has none
-      s += e * t.y;
-      u += e * (t.z + d * t.y);
+    if (t.x != -INFINITY || t.y != 0.f || t.z != 0.f) {  // a half tile without a column has none
+      const float d = t.x - m;
+      const double e = (double)tc::ex2(d);
+      s += e * (double)t.y;
+      u += e * ((double)t.z + (double)d * (double)t.y);
     }
   }
 #pragma unroll
@@ -256,8 +458,8 @@ head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
     u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
   }
   if (lane != 0) return;
-  const double log2s = log2((double)s);
-  if (entropy) entropy[row] = (float)(kLn2 * (log2s - (double)u / (double)s));
+  const double log2s = log2(s);
+  if (entropy) entropy[row] = (float)(kLn2 * (log2s - u / s));
   if (logprob) {
     const int32_t t = a.targets[row];
     float v = __uint_as_float(0x7FC00000u);
@@ -268,15 +470,21 @@ head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
   }
 }
 
-// Ranges of W's rows for `rows` rows: one CTA of every SM for up to 128 rows, then the smallest
-// count that fills whole waves of the 148 SMs to 97% (at most 32 per row tile).
+// Pairs from the 129th row on: one CTA a tile reads twice the bytes of W for the rows of two.
+bool head_pairs(int64_t rows) { return rows > kBM; }
+
+// Ranges of W's rows: one for every CTA or pair of the machine for one row tile, else the smallest
+// count that fills whole waves of them to 97% (at most 32 per row tile).
 int head_splits(int64_t rows, int64_t vocab) {
-  const int64_t units = (vocab + kUnit - 1) / kUnit, m = (rows + kBM - 1) / kBM;
+  const bool pairs = head_pairs(rows);
+  const int64_t unit = pairs ? HeadCfg<true>::kUnit : HeadCfg<false>::kUnit;
+  const int64_t tile = pairs ? HeadCfg<true>::kRows : HeadCfg<false>::kRows, slots = pairs ? kSmCount / 2 : kSmCount;
+  const int64_t units = (vocab + unit - 1) / unit, m = (rows + tile - 1) / tile;
   int64_t best = 1;
   double fill = 0.0;
-  const int64_t most = m * 32 < kSmCount ? kSmCount / m : 32;
+  const int64_t most = m * 32 < slots ? slots / m : 32;
   for (int64_t s = 1; s <= most && s <= units; ++s) {
-    const double waves = (double)(m * s) / kSmCount, f = waves / std::ceil(waves);
+    const double waves = (double)(m * s) / slots, f = waves / std::ceil(waves);
     if (f > fill + 1e-9) {
       fill = f;
       best = s;
@@ -330,27 +538,44 @@ zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64
   const DeviceScope device(ctx);
   if (device.status != cudaSuccess)
     return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
-  CUtensorMap ta, tb;
-  if (!tile_map_bf16(&ta, hidden, rows, width, ldh, kBM) || !tile_map_bf16(&tb, W, vocab, width, ldw, kUnit))
-    return fail(ctx, ZO_ERR_CUDA, "head_logprobs: cuTensorMapEncodeTiled failed");
+  const bool pairs = head_pairs(rows);
+  const int unit = pairs ? HeadCfg<true>::kUnit : HeadCfg<false>::kUnit;
   HeadArgs a;
   a.rows = (int)rows;
   a.vocab = (int)vocab;
   a.width = (int)width;
   a.splits = head_splits(rows, vocab);
-  a.units = (int)((vocab + kUnit - 1) / kUnit);
+  a.units = (int)((vocab + unit - 1) / unit);
+  a.a_rows = rows < kBM ? (int)(rows + 7) / 8 * 8 : kBM;
   a.targets = targets;
   a.part = static_cast<float4 *>(workspace);
   a.target_logit = reinterpret_cast<float *>(a.part + rows * 2 * a.splits);
   a.err = &ctx->dstate->flags;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(head_kernel), (int)HeadSmem::kBytes);
+  CUtensorMap ta, tb;
+  if (!tile_map_bf16(&ta, hidden, rows, width, ldh, a.a_rows) || !tile_map_bf16(&tb, W, vocab, width, ldw, kBox))
+    return fail(ctx, ZO_ERR_CUDA, "head_logprobs: cuTensorMapEncodeTiled failed");
+  auto kernel = pairs ? head_pair_kernel : head_kernel;
+  const int smem = (int)(pairs ? HeadCfg<true>::kBytes : HeadCfg<false>::kBytes);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_kernel attribute: %s", cudaGetErrorString(e));
-  const dim3 grid((unsigned)((rows + kBM - 1) / kBM), (unsigned)a.splits);
-  head_kernel<<<grid, kThreads, HeadSmem::kBytes, ctx->stream>>>(ta, tb, a);
+  const int64_t m = (rows + kBM - 1) / kBM;
+  const dim3 grid((unsigned)(pairs ? (m + 1) / 2 * 2 : m), (unsigned)a.splits);
+  kernel<<<grid, kThreads, smem, ctx->stream>>>(ta, tb, a);
   zo_status st = check_launch(ctx, "head_kernel");
   if (st != ZO_OK) return st;
-  head_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, ctx->stream>>>(a, logprob, entropy);
-  return check_launch(ctx, "head_join_kernel");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = ctx->stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, head_join_kernel, a, logprob, entropy);
+  if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_join_kernel: %s", cudaGetErrorString(e));
+  ctx->launches += 1;
+  return ZO_OK;
 }
 
 }  // extern "C"

@@ -142,13 +142,6 @@ __device__ __forceinline__ void add_scale2(float a0, float a1, float b, float c,
       "add.rn.f32x2 a, a, b;\n\tmul.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
-// (u0, u1) += (a0, a1) * (b0, b1)
-__device__ __forceinline__ void fma2(float &u0, float &u1, float a0, float a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 u, a, b;\n\t"
-      "mov.b64 u, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "fma.rn.f32x2 u, a, b, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
-      : "+f"(u0), "+f"(u1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
 
 // Descending bitonic sort of one key per lane.
 __device__ __forceinline__ uint64_t warp_sort(uint64_t k) {
@@ -274,7 +267,7 @@ struct Scan {
         constexpr int kPairs = 2;
         const int h = (i / 2) % kPairs * 2;
         tc::add2(s[h], s[h + 1], p0, p1);
-        fma2(u[h], u[h + 1], p0, p1, t0, t1);
+        tc::fma2(u[h], u[h + 1], p0, p1, t0, t1);
       }
     }
     return all;

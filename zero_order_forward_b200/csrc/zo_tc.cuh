@@ -123,6 +123,14 @@ __device__ __forceinline__ void add2(float &s0, float &s1, float a0, float a1) {
       : "+f"(s0), "+f"(s1) : "f"(a0), "f"(a1));
 }
 
+// (u0, u1) += (a0, a1) * (b0, b1)
+__device__ __forceinline__ void fma2(float &u0, float &u1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 u, a, b;\n\t"
+      "mov.b64 u, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "fma.rn.f32x2 u, a, b, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(u0), "+f"(u1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // All lanes of the warp wait for `parity` on `bar`: lane 0 decides (bounded), then every lane
 // observes the completed phase.  Returns false (on every lane) on expiry or abort.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
