@@ -27,7 +27,7 @@ constexpr float kLog2E = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kBox = 32;  // rows of W in one TMA box
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;  // 4 for each quarter of a tile's columns: the exponentials need warps to wait for
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 
 template <bool PAIR>
@@ -39,7 +39,8 @@ struct HeadCfg {
   static constexpr uint32_t kBBytes = (PAIR ? kBN / 2 : kBN) * kBK * 2;
   static constexpr uint32_t kBoxBytes = kBox * kBK * 2;
   static constexpr uint32_t kBarOffset = kStages * (kABytes + kBBytes);
-  static constexpr uint32_t kBytes = kBarOffset + 256 + 1024;
+  static constexpr uint32_t kStatsOffset = kBarOffset + 256;  // RowStats [quarter][128]
+  static constexpr uint32_t kBytes = kStatsOffset + (kEpiWarps / 4) * kBM * 24 + 1024;
   static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barrier area");
 };
 
@@ -49,7 +50,7 @@ struct HeadArgs {
   int units;              // of W's rows
   int a_rows;             // rows of a box of `hidden` (a multiple of 8; those behind are not loaded)
   const int32_t *targets; // may be null
-  float4 *part;           // [rows][2 splits] (m, s, u, -)
+  float4 *part;           // [rows][splits] (m, s, u, -)
   float *target_logit;    // [rows]
   uint32_t *err;
 };
@@ -66,6 +67,17 @@ __device__ __forceinline__ int range_first(int i, int units, int splits, int uni
 struct RowStats {
   float m = -INFINITY;
   double s = 0.0, u = 0.0;
+
+  // Nothing seen.
+  __device__ __forceinline__ bool empty() const { return m == -INFINITY && s == 0.0 && u == 0.0; }
+  // These sums relative to `top` (a whole number, m at least), added to (s, u) there.
+  __device__ __forceinline__ void add_to(float top, double &ts, double &tu) const {
+    if (empty()) return;
+    const float d = m - top;
+    const double e = (double)tc::ex2(d);
+    ts += e * s;
+    tu += e * (u + (double)d * s);
+  }
 
   __device__ __forceinline__ void take(const float (&v)[32]) {
     float x4[4] = {v[0], v[1], v[2], v[3]};
@@ -101,6 +113,18 @@ struct RowStats {
   }
 };
 
+static_assert(sizeof(RowStats) == 24, "HeadCfg::kBytes");
+
+// The triple of one row over a CTA's columns, from those of its quarters (kBM apart).
+__device__ __forceinline__ void write_part(const HeadArgs &a, const RowStats *quarter, int row, int split) {
+  RowStats r;
+#pragma unroll
+  for (int k = 0; k < kEpiWarps / 4; ++k) r.m = fmaxf(r.m, quarter[k * kBM].m);
+#pragma unroll
+  for (int k = 0; k < kEpiWarps / 4; ++k) quarter[k * kBM].add_to(r.m, r.s, r.u);
+  a.part[(int64_t)row * a.splits + split] = make_float4(r.m, (float)r.s, (float)r.u, 0.f);
+}
+
 // The columns [c0, c0 + 32) of the tile at W's row n0 (`cols` of them exist) of one row.
 __device__ __forceinline__ void take_chunk(RowStats &st, uint32_t taddr, int n0, int c0, int cols, int target,
                                            float *target_logit) {
@@ -135,6 +159,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   uint64_t *mma_done = acc_empty + 2;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  RowStats *stats = reinterpret_cast<RowStats *>(smem + S::kStatsOffset);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.x * kBM, split = blockIdx.y;
@@ -220,7 +245,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
     tc::mma_commit(mma_done);  // arrives once every MMA issued above has retired
   } else if (warp >= 2) {
-    const int q = warp & 3, half = (warp - 2) / 4;  // TMEM lane quadrant; half of the columns
+    const int q = warp & 3, quarter = (warp - 2) / 4;  // TMEM lane quadrant; quarter of the columns
     const int row = m0 + 32 * q + lane;
     const int target = a.targets && row < a.rows ? a.targets[row] : -1;
     const bool any = m0 + 32 * q < a.rows;  // a warp without a row only passes the accumulators on
@@ -237,7 +262,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
       if (any) {
 #pragma unroll 1
-        for (int c0 = half * (kBN / 2); c0 < min(cols, (half + 1) * (kBN / 2)); c0 += 32)
+        for (int c0 = quarter * (kBN / 4); c0 < min(cols, (quarter + 1) * (kBN / 4)); c0 += 32)
           take_chunk(st, base, n0, c0, cols, target, a.target_logit + row);
       }
       tc::tc_fence_before();
@@ -248,11 +273,11 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       atomicOr(a.err, ZO_FLAG_TIMEOUT);
       *abort_flag = 1;
     }
-    if (row < a.rows)
-      a.part[(int64_t)row * (2 * a.splits) + 2 * split + half] = make_float4(st.m, (float)st.s, (float)st.u, 0.f);
+    stats[quarter * kBM + 32 * q + lane] = st;
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x < kBM && m0 + (int)threadIdx.x < a.rows) write_part(a, stats + threadIdx.x, m0 + threadIdx.x, split);
   if (warp == 0 && lane == 0 && *abort_flag) {
     // let this CTA's TMA loads still in flight land before it exits (bounded)
     for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
@@ -286,6 +311,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   uint64_t *mma_done = acc_empty + 2;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  RowStats *stats = reinterpret_cast<RowStats *>(smem + S::kStatsOffset);
 
   const uint32_t rank = tc::cluster_ctarank();
   const bool leader = rank == 0;
@@ -378,7 +404,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     tc::mma_commit_pair(mma_done);  // arrives (in both CTAs) once every MMA above has retired
   } else if (warp >= 2) {
-    const int q = warp & 3, half = (warp - 2) / 4;
+    const int q = warp & 3, quarter = (warp - 2) / 4;
     const int row = m0 + 32 * q + lane;
     const int target = a.targets && row < a.rows ? a.targets[row] : -1;
     const bool any = m0 + 32 * q < a.rows;
@@ -394,7 +420,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
       if (any) {
 #pragma unroll 1
-        for (int c0 = half * (kBN / 2); c0 < min(cols, (half + 1) * (kBN / 2)); c0 += 32)
+        for (int c0 = quarter * (kBN / 4); c0 < min(cols, (quarter + 1) * (kBN / 4)); c0 += 32)
           take_chunk(st, base, n0, c0, cols, target, a.target_logit + row);
       }
       tc::tc_fence_before();
@@ -404,11 +430,11 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         else tc::mbar_arrive_remote(acc_empty_leader + 8u * (uint32_t)b);
       }
     }
-    if (row < a.rows)
-      a.part[(int64_t)row * (2 * a.splits) + 2 * split + half] = make_float4(st.m, (float)st.s, (float)st.u, 0.f);
+    stats[quarter * kBM + 32 * q + lane] = st;
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x < kBM && m0 + (int)threadIdx.x < a.rows) write_part(a, stats + threadIdx.x, m0 + threadIdx.x, split);
   if (warp == 0 && lane == 0 && *abort_flag) {
     if (leader) {
       // let the pair's loads still in flight land before either CTA exits (bounded)
@@ -434,23 +460,32 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 // One warp per row: its triples joined lane by lane, then across the lanes, in fp64.
 __global__ void __launch_bounds__(256)
 head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
+  constexpr int N = (kSmCount + 31) / 32;  // triples of a lane (148 at most in all)
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   tc::pdl_wait();
   if (row >= a.rows) return;
-  const float4 *part = a.part + (int64_t)row * (2 * a.splits);
+  const float4 *part = a.part + (int64_t)row * a.splits;
+  const int32_t target = logprob ? a.targets[row] : -1;
+  const float target_logit = a.target_logit[row];  // not written without a target in range
+  float4 t[N];
   float m = -INFINITY;
-  for (int i = lane; i < 2 * a.splits; i += 32) m = fmaxf(m, part[i].x);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    t[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    if (lane + 32 * k < a.splits) t[k] = part[lane + 32 * k];
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) m = fmaxf(m, t[k].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   double s = 0.0, u = 0.0;
-  for (int i = lane; i < 2 * a.splits; i += 32) {
-    const float4 t = part[i];
-    if (t.x != -INFINITY || t.y != 0.f || t.z != 0.f) {  // a half tile without a column has none
-      const float d = t.x - m;
-      const double e = (double)tc::ex2(d);
-      s += e * (double)t.y;
-      u += e * ((double)t.z + (double)d * (double)t.y);
-    }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    RowStats r;
+    r.m = t[k].x;
+    r.s = (double)t[k].y;
+    r.u = (double)t[k].z;
+    r.add_to(m, s, u);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -461,11 +496,10 @@ head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
   const double log2s = log2(s);
   if (entropy) entropy[row] = (float)(kLn2 * (log2s - u / s));
   if (logprob) {
-    const int32_t t = a.targets[row];
     float v = __uint_as_float(0x7FC00000u);
-    if (t == -1) v = 0.f;
-    else if (t >= 0 && t < a.vocab)
-      v = (float)(kLn2 * ((double)a.target_logit[row] * (double)kLog2E - (double)m - log2s));
+    if (target == -1) v = 0.f;
+    else if (target >= 0 && target < a.vocab)
+      v = (float)(kLn2 * ((double)target_logit * (double)kLog2E - (double)m - log2s));
     logprob[row] = v;
   }
 }
@@ -473,23 +507,38 @@ head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
 // Pairs from the 129th row on: one CTA a tile reads twice the bytes of W for the rows of two.
 bool head_pairs(int64_t rows) { return rows > kBM; }
 
-// Ranges of W's rows: one for every CTA or pair of the machine for one row tile, else the smallest
-// count that fills whole waves of them to 97% (at most 32 per row tile).
-int head_splits(int64_t rows, int64_t vocab) {
+struct HeadShape {
+  int64_t unit, row_tiles, slots, units;
+  int64_t most;  // ranges: one for every CTA or pair of the machine for one row tile, at most 32 for more
+};
+HeadShape head_shape(int64_t rows, int64_t vocab) {
   const bool pairs = head_pairs(rows);
-  const int64_t unit = pairs ? HeadCfg<true>::kUnit : HeadCfg<false>::kUnit;
-  const int64_t tile = pairs ? HeadCfg<true>::kRows : HeadCfg<false>::kRows, slots = pairs ? kSmCount / 2 : kSmCount;
-  const int64_t units = (vocab + unit - 1) / unit, m = (rows + tile - 1) / tile;
+  const int64_t tile = pairs ? HeadCfg<true>::kRows : HeadCfg<false>::kRows;
+  HeadShape h;
+  h.unit = pairs ? HeadCfg<true>::kUnit : HeadCfg<false>::kUnit;
+  h.slots = pairs ? kSmCount / 2 : kSmCount;
+  h.row_tiles = (rows + tile - 1) / tile;
+  h.units = (vocab + h.unit - 1) / h.unit;
+  h.most = h.row_tiles * 32 < h.slots ? h.slots / h.row_tiles : 32;
+  if (h.most > h.units) h.most = h.units;
+  return h;
+}
+
+// The number of ranges whose estimated time is least: waves of CTAs (or pairs), each a fixed cost
+// (start, first loads, last epilogue: about 4 us) and its units' products (9 TFLOP/s an
+// SM) or exponentials (16 a clock).
+int head_splits(const HeadShape &h, int64_t width) {
+  const double flops = 2.0 * kBM * (double)h.unit * (double)((width + kBK - 1) / kBK * kBK);
+  const double unit_us = std::fmax(flops / 9.0e6, kBM * (double)h.unit / 16.0 / 1.8e3);
   int64_t best = 1;
-  double fill = 0.0;
-  const int64_t most = m * 32 < slots ? slots / m : 32;
-  for (int64_t s = 1; s <= most && s <= units; ++s) {
-    const double waves = (double)(m * s) / slots, f = waves / std::ceil(waves);
-    if (f > fill + 1e-9) {
-      fill = f;
+  double least = 1e300;
+  for (int64_t s = 1; s <= h.most; ++s) {
+    const int64_t waves = (h.row_tiles * s + h.slots - 1) / h.slots;
+    const double us = (double)waves * (4.0 + unit_us * (double)((h.units + s - 1) / s));
+    if (us < least * 0.995) {
+      least = us;
       best = s;
     }
-    if (m > 1 && fill >= 0.97) break;
   }
   return (int)best;
 }
@@ -499,7 +548,7 @@ bool head_sizes_ok(int64_t rows, int64_t vocab) {
 }
 
 int64_t head_bytes(int64_t rows, int64_t vocab) {
-  return rows * (2 * (int64_t)head_splits(rows, vocab) * (int64_t)sizeof(float4)) + ((rows * 4 + 15) / 16) * 16;
+  return rows * (head_shape(rows, vocab).most * (int64_t)sizeof(float4)) + ((rows * 4 + 15) / 16) * 16;
 }
 
 }  // namespace
@@ -539,17 +588,17 @@ zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64
   if (device.status != cudaSuccess)
     return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
   const bool pairs = head_pairs(rows);
-  const int unit = pairs ? HeadCfg<true>::kUnit : HeadCfg<false>::kUnit;
+  const HeadShape shape = head_shape(rows, vocab);
   HeadArgs a;
   a.rows = (int)rows;
   a.vocab = (int)vocab;
   a.width = (int)width;
-  a.splits = head_splits(rows, vocab);
-  a.units = (int)((vocab + unit - 1) / unit);
+  a.splits = head_splits(shape, width);
+  a.units = (int)shape.units;
   a.a_rows = rows < kBM ? (int)(rows + 7) / 8 * 8 : kBM;
   a.targets = targets;
   a.part = static_cast<float4 *>(workspace);
-  a.target_logit = reinterpret_cast<float *>(a.part + rows * 2 * a.splits);
+  a.target_logit = reinterpret_cast<float *>(a.part + rows * a.splits);
   a.err = &ctx->dstate->flags;
   CUtensorMap ta, tb;
   if (!tile_map_bf16(&ta, hidden, rows, width, ldh, a.a_rows) || !tile_map_bf16(&tb, W, vocab, width, ldw, kBox))
