@@ -3,15 +3,25 @@
 //
 //   out_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   over the rows j of i's own sequence.
 //
-// One CTA (6 warps) per (128-query tile of one sequence, head), two CTAs per SM.  The grid holds
-// as many blocks as tiles are possible (ceil(total / 128) + n_seqs); a block finds its sequence
-// and tile by counting tiles over cu_seqlens, which is read on the device only.  Key tiles of 64
-// keys flow through the pipeline of zo_attn_tc.cu: one warp issues TMA loads, one the MMAs
-// (S = Q K^T into tensor memory, O += P V with P read from tensor memory), four compute the
-// softmax, one query row per thread.  What packing adds:
+// One CTA of 12 warps per SM takes items, one after another: two streams of 128 query rows each that
+// share key and value tiles of 128 keys,
+//   kHeads  two query heads of one key/value head (an even number of them share it),
+//   kPair64 two heads of dim 64 with their own key/value heads, which lie side by side in the rows,
+//   kRows   256 rows of one head otherwise.
+// A warp issues the TMA loads, one the MMAs (S = Q K^T into tensor memory, O += P V with P read from
+// tensor memory, where it replaces S), and four per stream compute the softmax, one query row per
+// thread: while one stream's exponentials run, the tensor cores work on the other's products.  Two
+// streams of 128 x 128 scores take all 512 columns of tensor memory (hd 128).
+//
+// Items are numbered by falling length (the number of key tiles), heads fastest; CTA c takes item
+// c of every round of gridDim.x, in turn from the front and from the back, so that the CTAs' sums
+// differ little.  cu_seqlens is read on the device only: one warp counts the sequences that have a
+// query tile of the length in turn and hands the items on.
+//
+// What packing adds:
 //   - tiles start at any row, so the last key tile of a sequence also holds rows of the next one
-//     (or padding): their scores are masked, their value rows cleared in shared memory before
-//     they are multiplied;
+//     (or padding): their scores are masked, groups of 16 keys behind the sequence are not
+//     multiplied, and value rows behind it in its last group are cleared in shared memory;
 //   - within the diagonal tile a later token's value row is multiplied by probability 0, which is
 //     not 0 for an infinity or NaN: a row whose output is not finite is looked at again
 //     (repair_rows) and recomputed from its own keys alone where a later row is to blame.
@@ -28,32 +38,27 @@ using tc::ex2;
 using tc::fma2_bc;
 using tc::max3f;
 using tc::ring_parity;
-using tc::warp_wait;
 
-constexpr int kTBM = 128, kTThreads = 192;
-constexpr uint32_t kQBox = 128 * 128;  // bytes of one 128-row x 64-column bf16 box
+constexpr int kM = 128;                // query rows of a stream, keys of a tile
+constexpr int kWarps = 12;             // loads, MMAs, items, an idle one; 2 x 4 softmax
+constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kBox = kM * 128;    // bytes of one 128-row x 64-column bf16 box
+constexpr int kItems = 2;              // items on hand
 
-template <int HD> struct PackedCfg {
-  static constexpr int kBN = 64;
-  static constexpr int kKS = HD == 128 ? 2 : 4;  // K stages
-  static constexpr int kVS = HD == 128 ? 2 : 4;  // V stages
-  static constexpr int kCtas = 2;
-  static constexpr int kTmemCols = 256;
-  static constexpr uint32_t kKBox = kBN * 128;  // bytes of one kBN-row x 64-column bf16 box
-};
+enum Mode { kHeads, kPair64, kRows };
 
-template <int HD>
+template <int HD, bool SPLIT>  // SPLIT: the streams have key/value heads of their own (kPair64)
 struct PackedSmem {
-  static constexpr int kKS = PackedCfg<HD>::kKS, kVS = PackedCfg<HD>::kVS;
-  static constexpr uint32_t kQTile = (HD / 64) * kQBox;
-  static constexpr uint32_t kKTile = (HD / 64) * PackedCfg<HD>::kKBox;
+  static constexpr uint32_t kQTile = (HD / 64) * kBox;                     // of one stream
+  static constexpr uint32_t kStage = (SPLIT ? 2 : HD / 64) * kBox;         // one key or value tile
+  static constexpr int kStages = HD == 128 ? 5 : SPLIT ? 6 : 10;
   static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = kQ + kQTile;        // [kKS]
-  static constexpr uint32_t kV = kK + kKS * kKTile;  // [kVS]
-  static constexpr uint32_t kBar = kV + kVS * kKTile;
-  static constexpr int kNumBars = 1 + 2 * kKS + 2 * kVS + 2 + 2 + 2 + 1;
-  static constexpr uint32_t kBytes = kBar + 256 + 1024;  // barriers + alignment slack
-  static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
+  static constexpr uint32_t kKV = 2 * kQTile;
+  static constexpr uint32_t kBar = kKV + kStages * kStage;
+  static constexpr int kNumBars = 2 * kStages + 2 + 8 + 2 * kItems + 1;
+  static constexpr uint32_t kItem = kBar + 8 * ((kNumBars + 2) / 2 * 2);   // Item [kItems]
+  static constexpr uint32_t kBytes = kItem + kItems * 32 + 1024;           // + alignment slack
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct PackedArgs {
@@ -63,52 +68,109 @@ struct PackedArgs {
   int n_seqs, total, H, Hk;
   int64_t ldq, ldk, ldv, ldo;
   float scale_log2;
+  int mode;
   uint32_t *err;
 };
 
-struct Tile {
-  int row0, len;  // the sequence's first row and length (0: no such tile)
-  int qt;         // query tile within the sequence
+struct Item {
+  int row0, len;   // the sequence's first row and length (0: no more items)
+  int qt;          // tile of the item (of 128 rows, or 256: kRows) within the sequence
+  int head;        // stream 0's query head
 };
 
-// The sequence and query tile of tile number `slot`, counting ceil(len / 128) tiles for every
-// sequence in order.  All threads of the block call; each warp counts by itself, 32 sequences at a
-// time.  Pairs of offsets that decrease or leave [0, total] count no tile; `check` goes on to the
-// last one and raises ZO_FLAG_OFFSETS for them.
-__device__ __forceinline__ Tile find_tile(const PackedArgs &a, int slot, bool check) {
-  const int lane = threadIdx.x & 31;
-  Tile t{0, 0, 0};
-  int base = 0;
-  for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
-    const int i = i0 + lane;
-    int s = 0, e = 0;
-    if (i < a.n_seqs) {
-      s = __ldg(a.cu + i);
-      e = __ldg(a.cu + i + 1);
-      if (s < 0 || e < s || e > a.total) {
-        if (check && threadIdx.x < 32) atomicOr(a.err, ZO_FLAG_OFFSETS);
-        s = e = 0;
-      }
-    }
-    const int n = (e - s + kTBM - 1) / kTBM;
-    int incl = n;
+// What the streams of an item do, from the item.
+struct Work {
+  int row0, len, kvh;
+  int q[2], head[2], keys[2], tiles[2];  // first query row, head, keys and key tiles (0: no such stream)
+  int most;                              // key tiles of the longer stream
+  __device__ __forceinline__ Work(const PackedArgs &a, const Item &it) {
+    row0 = it.row0;
+    len = it.len;
+    const bool rows = a.mode == kRows;
+    kvh = it.head / (a.H / a.Hk);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
+    for (int i = 0; i < 2; ++i) {
+      q[i] = rows ? 2 * kM * it.qt + kM * i : kM * it.qt;
+      head[i] = rows ? it.head : it.head + i;
+      keys[i] = q[i] < len ? min(q[i] + kM, len) : 0;
+      tiles[i] = (keys[i] + kM - 1) / kM;
     }
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + incl > slot);
-    if (past && t.len == 0) {
-      const int l = __ffs(past) - 1;
-      t.row0 = __shfl_sync(0xFFFFFFFFu, s, l);
-      t.len = __shfl_sync(0xFFFFFFFFu, e, l) - t.row0;
-      t.qt = slot - (base + __shfl_sync(0xFFFFFFFFu, incl - n, l));
-      if (!check) break;
-    }
-    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    most = max(tiles[0], tiles[1]);
   }
-  return t;
+  // The last tile's value rows behind the sequence share a group of 16 with its own.
+  __device__ __forceinline__ bool ragged() const { return most * kM >= len && len % 16 != 0; }
+};
+
+// Tiles of `per` rows of sequence i; 0 if it is empty or its offsets decrease or leave [0, total].
+__device__ __forceinline__ int seq_tiles(const PackedArgs &a, int i, int per, bool &bad) {
+  bad = false;
+  if (i >= a.n_seqs) return 0;
+  const int s = __ldg(a.cu + i), e = __ldg(a.cu + i + 1);
+  bad = s < 0 || e < s || e > a.total;
+  return bad ? 0 : (int)(((int64_t)e - s + per - 1) / per);
 }
+
+// The items of one CTA in their order (one warp).
+struct Schedule {
+  const PackedArgs &a;
+  int per, group;          // rows of a tile; items of one tile (heads, or pairs of them)
+  int lane, first_tiles;   // this lane's count of the first 32 sequences
+  int level, count;        // sequences with more than `level` tiles: `count`
+  int64_t base;            // items of the longer levels
+  __device__ __forceinline__ Schedule(const PackedArgs &args) : a(args) {
+    lane = threadIdx.x & 31;
+    per = a.mode == kRows ? 2 * kM : kM;
+    group = a.mode == kRows ? a.H : a.H / 2;
+    int most = 0, any_bad = 0;
+    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
+      bool bad;
+      const int n = seq_tiles(a, i0 + lane, per, bad);
+      if (i0 == 0) first_tiles = n;
+      most = max(most, n);
+      any_bad |= bad;
+    }
+    if (blockIdx.x == 0 && any_bad) atomicOr(a.err, ZO_FLAG_OFFSETS);
+    level = __reduce_max_sync(0xFFFFFFFFu, most) - 1;
+    base = 0;
+    count = level >= 0 ? sequences() : 0;
+  }
+  __device__ __forceinline__ bool has(int i0) const {
+    bool bad;
+    return (i0 == 0 ? first_tiles : seq_tiles(a, i0 + lane, per, bad)) > level;
+  }
+  __device__ __forceinline__ int sequences() const {
+    int n = 0;
+    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, has(i0)));
+    return n;
+  }
+  // Item `slot`; slots must not decrease from call to call.
+  __device__ __forceinline__ Item at(int64_t slot) {
+    while (level >= 0 && slot >= base + (int64_t)count * group) {
+      base += (int64_t)count * group;
+      --level;
+      if (level >= 0) count = sequences();
+    }
+    Item it{0, 0, 0, 0};
+    if (level < 0) return it;
+    const int index = (int)(slot - base);
+    int nth = index / group;
+    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, has(i0));
+      const int n = __popc(in);
+      if (nth < n) {
+        const uint32_t lower = in & ((1u << lane) - 1u);
+        const int i = i0 + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && __popc(lower) == nth)) - 1;
+        it.row0 = __ldg(a.cu + i);
+        it.len = __ldg(a.cu + i + 1) - it.row0;
+        it.qt = level;
+        it.head = (index - index / group * group) * (a.mode == kRows ? 1 : 2);
+        break;
+      }
+      nth -= n;
+    }
+    return it;
+  }
+};
 
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
 
@@ -117,20 +179,20 @@ __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) !
 // (up to key_end) does.  One warp: a row with a non-finite later value row, and with a non-finite
 // output that no own key's value explains, is computed again from keys 0 .. r alone, in fp32.
 template <int HD>
-__device__ __noinline__ void repair_rows(const PackedArgs &a, const Tile &tile, int first, uint32_t rows,
+__device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len, int first, uint32_t rows,
                                          int h, int kvh, int key_end) {
   constexpr int C = HD / 32;  // output columns of a lane: C lane .. C lane + C - 1
   const int lane = threadIdx.x & 31;
-  const uint16_t *K = a.k + (int64_t)tile.row0 * a.ldk + kvh * HD;
-  const uint16_t *V = a.v + (int64_t)tile.row0 * a.ldv + kvh * HD + C * lane;
+  const uint16_t *K = a.k + (int64_t)row0 * a.ldk + kvh * HD;
+  const uint16_t *V = a.v + (int64_t)row0 * a.ldv + kvh * HD + C * lane;
   for (; rows; rows &= rows - 1) {
     const int r = first + __ffs(rows) - 1;
     bool later = false;
-    for (int j = r + 1; j < min(key_end, tile.len); ++j)
+    for (int j = r + 1; j < min(key_end, len); ++j)
 #pragma unroll
       for (int c = 0; c < C; ++c) later |= !finite_bf16(V[(int64_t)j * a.ldv + c]);
     if (!__any_sync(0xFFFFFFFFu, later)) continue;
-    uint16_t *orow = a.out + (int64_t)(tile.row0 + r) * a.ldo + h * HD + C * lane;
+    uint16_t *orow = a.out + (int64_t)(row0 + r) * a.ldo + h * HD + C * lane;
     uint32_t open = 0;  // this lane's non-finite outputs not explained yet
 #pragma unroll
     for (int c = 0; c < C; ++c) open |= finite_bf16(orow[c]) ? 0u : 1u << c;
@@ -139,7 +201,7 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, const Tile &tile, 
       for (int c = 0; c < C; ++c)
         if (!finite_bf16(V[(int64_t)j * a.ldv + c])) open &= ~(1u << c);
     if (!__any_sync(0xFFFFFFFFu, open)) continue;
-    const uint16_t *q = a.q + (int64_t)(tile.row0 + r) * a.ldq + h * HD;
+    const uint16_t *q = a.q + (int64_t)(row0 + r) * a.ldq + h * HD;
     float m = -INFINITY, l = 0.f, acc[C] = {};
     for (int j0 = 0; j0 <= r; j0 += 32) {
       const int j = j0 + lane;
@@ -175,43 +237,98 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, const Tile &tile, 
   }
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kTThreads, PackedCfg<HD>::kCtas)
+// One row's step over the first 32 NC keys of a tile: its scores from tensor memory at tS, maximum,
+// probabilities back to the first 16 NC columns there, sum.  MASK: keys behind `last` do not count
+// (their scores may be anything).
+template <int HD, int NC, bool MASK>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale_log2, bool first, int last,
+                                             float &m_used, float &l) {
+  float s[32 * NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) tc::tmem_ld32_async(tS + 32u * c, s + 32 * c);
+  tc::tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < NC; ++c) tc::tmem_ld_seal(s + 32 * c);
+  if (MASK) {
+#pragma unroll
+    for (int e = 0; e < 32 * NC; ++e)
+      if (e > last) s[e] = -INFINITY;
+  }
+  // the maximum of the raw scores (the scale is positive), then 2^(s * scale - m) with the
+  // scaling folded into the exponent's fused multiply-add
+  float mx8[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 32 * NC; e += 2) mx8[(e >> 1) & 7] = max3f(mx8[(e >> 1) & 7], s[e], s[e + 1]);
+  const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale_log2;
+  const float m_new = fmaxf(m_used, mx);
+  // Lazy rescaling: keep the running maximum unless it grows by more than 2^8 (then O and l
+  // are rescaled; P_{j-1} V_{j-1} has completed, as S_j was issued after it).
+  const bool need = !first && m_new > m_used + 8.f;
+  if (__any_sync(0xFFFFFFFFu, need)) {
+    const float f = need ? ex2(m_used - m_new) : 1.f;
+    l *= f;
+#pragma unroll 1
+    for (int c = 0; c < HD / 16; ++c) {
+      float o[16];
+      tc::tmem_ld16(tO + 16u * c, o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] *= f;
+      tc::tmem_st16(tO + 16u * c, o);
+    }
+  }
+  if (first || need) m_used = m_new;
+  const float msc = m_used == -INFINITY ? 0.f : m_used;
+  float ls4[4] = {0.f, 0.f, 0.f, 0.f};  // two packed pairs of partial sums
+  // P_j overwrites columns of S_j (already read into registers)
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float x0, x1;
+      fma2_bc(s[32 * c + e], s[32 * c + e + 1], scale_log2, -msc, x0, x1);
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      if ((e >> 1) & 1) add2(ls4[2], ls4[3], p0, p1);
+      else add2(ls4[0], ls4[1], p0, p1);
+      pk[e / 2] = pack_bf16x2(p0, p1);
+    }
+    tc::tmem_st16u_async(tS + 16u * c, pk);
+  }
+  l += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+  tc::tmem_st_wait();
+}
+
+template <int HD, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
 attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                   const __grid_constant__ CUtensorMap tmv,
-                   PackedArgs a) {
-  using SM = PackedSmem<HD>;
-  constexpr int KS = SM::kKS, VS = SM::kVS;
-  constexpr uint32_t kCols = PackedCfg<HD>::kTmemCols;
-  constexpr int kTBN = PackedCfg<HD>::kBN;
-  constexpr uint32_t kKBox = PackedCfg<HD>::kKBox;
+                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PackedArgs a) {
+  using SM = PackedSmem<HD, SPLIT>;
+  constexpr int NS = SM::kStages;
+  constexpr uint32_t kCols = 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + SM::kBar);
-  uint64_t *q_full = bars;
-  uint64_t *k_full = q_full + 1, *k_empty = k_full + KS;
-  uint64_t *v_full = k_empty + KS, *v_empty = v_full + VS;
-  uint64_t *s_full = v_empty + VS;  // [2] scores of tile j in buffer j % 2
-  uint64_t *p_full = s_full + 2;    // [2] probabilities of tile j written (4 softmax warps)
-  uint64_t *pv_done = p_full + 2;   // [2] O += P_j V_j completed
-  uint64_t *mma_done = pv_done + 2;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + SM::kBar);  // [NS] ring of tiles K_0 V_0 K_1 V_1 ...
+  uint64_t *empty = full + NS;                                   // [NS]
+  uint64_t *q_full = empty + NS, *q_empty = q_full + 1;
+  uint64_t *s_full = q_empty + 1;   // [2] a stream's scores
+  uint64_t *p_full = s_full + 2;    // [2] its probabilities (4 warps)
+  uint64_t *pv_done = p_full + 2;   // [2] its O += P V
+  uint64_t *o_free = pv_done + 2;   // [2] its output has been read (4 warps)
+  uint64_t *item_full = o_free + 2, *item_empty = item_full + kItems;  // [kItems]
+  uint64_t *mma_done = item_empty + kItems;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  Item *items = reinterpret_cast<Item *>(sm + SM::kItem);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, kvh = h / (a.H / a.Hk);
-  const Tile tile = find_tile(a, blockIdx.x, blockIdx.x == 0 && h == 0);
-  if (tile.len == 0) return;  // more blocks than tiles (uniform over the block)
-  const int row0 = tile.row0, S = tile.len;
-  const int q_first = tile.qt * kTBM;
-  const int last_q = min(q_first + kTBM, S) - 1;
-  const int n_kt = last_q / kTBN + 1;
-
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SM::kNumBars; ++i) tc::mbar_init(&bars[i], 1);
-    tc::mbar_init(&p_full[0], 4);  // one arrival per softmax warp
-    tc::mbar_init(&p_full[1], 4);
+    for (int i = 0; i < SM::kNumBars; ++i) tc::mbar_init(&full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&p_full[i], 4);
+      tc::mbar_init(&o_free[i], 4);
+    }
+    for (int i = 0; i < kItems; ++i) tc::mbar_init(&item_empty[i], 2 + 8);  // loads, MMAs, softmax
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -219,221 +336,263 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  const uint32_t tO = tmem + 2 * kTBN;  // S/P buffers at columns 0 and kTBN
+  const uint32_t tmem = *tmem_holder;  // scores of stream i at column 128 i, output at 256 + HD i
 
-  if (warp == 0) {
-    if (lane == 0) {  // TMA producer: Q once, then K_j ahead of V_{j-1}
-      tc::tma_prefetch_desc(&tmq);
-      tc::tma_prefetch_desc(&tmk);
-      tc::tma_prefetch_desc(&tmv);
-      tc::mbar_arrive_expect_tx(q_full, SM::kQTile);
+  auto give_up = [&]() {
+    atomicOr(a.err, ZO_FLAG_TIMEOUT);
+    *abort_flag = 1;
+  };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return !*abort_flag && tc::mbar_wait(bar, parity); };
+  // Item n of this CTA, for one thread; one arrival on item_empty when it has been copied.
+  auto next_item = [&](int n, Item &it) {
+    if (!wait(&item_full[n % kItems], ring_parity(n, kItems))) return false;
+    it = items[n % kItems];
+    tc::mbar_arrive(&item_empty[n % kItems]);
+    return true;
+  };
+
+  // registers of a thread from here on: 4 warps x kFew + 8 x kMany = 12 x 168 of the launch
+  constexpr int kFew = 88, kMany = 208;
+  if (warp < 4) {
+    tc::regs_dec<kFew>();
+    if (warp == 0) {
+      int issued = 0;  // tiles of the ring
+      if (lane == 0) {
+        tc::tma_prefetch_desc(&tmq);
+        tc::tma_prefetch_desc(&tmk);
+        tc::tma_prefetch_desc(&tmv);
+        auto load = [&](const CUtensorMap &map, int kvh, int row) -> bool {
+          const int st = issued % NS;
+          if (!wait(&empty[st], ring_parity(issued, NS) ^ 1u)) return false;
+          tc::mbar_arrive_expect_tx(&full[st], SM::kStage);
 #pragma unroll
-      for (int c = 0; c < HD / 64; ++c)
-        tc::tma_load_2d(sm + SM::kQ + c * kQBox, &tmq, q_full, h * HD + 64 * c, row0 + q_first);
-      int k_issued = 0, v_issued = 0;
-      auto load_k = [&](int j) -> bool {
-        if (*abort_flag || !tc::mbar_wait(&k_empty[j % KS], ring_parity(j, KS) ^ 1u)) return false;
-        tc::mbar_arrive_expect_tx(&k_full[j % KS], SM::kKTile);
+          for (int c = 0; c < (int)(SM::kStage / kBox); ++c)
+            tc::tma_load_2d(sm + SM::kKV + st * SM::kStage + c * kBox, &map, &full[st], kvh * HD + 64 * c, row);
+          ++issued;
+          return true;
+        };
+        bool ok = true;
+        int n_q = 0;
+        for (int n = 0; ok; ++n) {
+          Item it;
+          ok = next_item(n, it);
+          if (!ok || it.len == 0) break;
+          const Work w(a, it);
+          ok = wait(q_empty, ((uint32_t)n & 1u) ^ 1u);
+          if (!ok) break;
+          n_q = n + 1;
+          tc::mbar_arrive_expect_tx(q_full, (w.tiles[1] ? 2 : 1) * SM::kQTile);
 #pragma unroll
-        for (int c = 0; c < HD / 64; ++c)
-          tc::tma_load_2d(sm + SM::kK + (j % KS) * SM::kKTile + c * kKBox, &tmk, &k_full[j % KS],
-                          kvh * HD + 64 * c, row0 + j * kTBN);
-        k_issued = j + 1;
-        return true;
-      };
-      auto load_v = [&](int j) -> bool {
-        if (*abort_flag || !tc::mbar_wait(&v_empty[j % VS], ring_parity(j, VS) ^ 1u)) return false;
-        tc::mbar_arrive_expect_tx(&v_full[j % VS], SM::kKTile);
-#pragma unroll
-        for (int c = 0; c < HD / 64; ++c)
-          tc::tma_load_2d(sm + SM::kV + (j % VS) * SM::kKTile + c * kKBox, &tmv, &v_full[j % VS],
-                          kvh * HD + 64 * c, row0 + j * kTBN);
-        v_issued = j + 1;
-        return true;
-      };
+          for (int i = 0; i < 2; ++i)
+            if (w.tiles[i])
+              for (int c = 0; c < HD / 64; ++c)
+                tc::tma_load_2d(sm + SM::kQ + i * SM::kQTile + c * kBox, &tmq, q_full, w.head[i] * HD + 64 * c,
+                                w.row0 + w.q[i]);
+          for (int j = 0; ok && j < w.most; ++j)
+            ok = load(tmk, w.kvh, w.row0 + j * kM) && load(tmv, w.kvh, w.row0 + j * kM);
+        }
+        if (!ok) {
+          give_up();
+          // let this CTA's loads land before it exits (bounded)
+          if (n_q > 0) tc::mbar_wait(q_full, (uint32_t)(n_q - 1) & 1u);
+          for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) tc::mbar_wait(&full[i % NS], ring_parity(i, NS));
+        }
+      }
+    } else if (warp == 1) {  // MMAs: the warp in step, one lane issues
+      const uint32_t sm0 = __shfl_sync(0xFFFFFFFFu, tc::smem_addr(sm), 0);
+      const uint32_t tm0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       bool ok = true;
-      for (int j = 0; ok && j <= n_kt; ++j) {
-        if (j < n_kt) ok = load_k(j);
-        if (ok && j >= 1) ok = load_v(j - 1);
-      }
-      if (!ok) {
-        atomicOr(a.err, ZO_FLAG_TIMEOUT);
-        *abort_flag = 1;
-        // let this CTA's loads land before it exits (bounded)
-        tc::mbar_wait(q_full, 0);
-        for (int i = k_issued - KS > 0 ? k_issued - KS : 0; i < k_issued; ++i)
-          tc::mbar_wait(&k_full[i % KS], ring_parity(i, KS));
-        for (int i = v_issued - VS > 0 ? v_issued - VS : 0; i < v_issued; ++i)
-          tc::mbar_wait(&v_full[i % VS], ring_parity(i, VS));
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {  // MMA issuer
-      constexpr uint32_t idS = tc::idesc_bf16_f32(kTBM, kTBN);
-      constexpr uint32_t idO = tc::idesc_bf16_f32(kTBM, HD) | (1u << 16);  // B (V) MN-major
-      const uint32_t qa = tc::smem_addr(sm + SM::kQ);
-      // S_j = Q K_j^T into score buffer j % 2
-      auto issue_s = [&](int j) -> bool {
-        if (*abort_flag || !tc::mbar_wait(&k_full[j % KS], ring_parity(j, KS))) return false;
-        tc::tc_fence_after();
-        const uint32_t ka = tc::smem_addr(sm + SM::kK + (j % KS) * SM::kKTile);
-        const uint32_t tS = tmem + (uint32_t)((j & 1) * kTBN);
+      uint32_t done[2] = {0, 0}, outs[2] = {0, 0};  // tiles and items of each stream so far
+      tc::RingPos<NS> key[2], val;                  // of the next key tile for each stream; of the value tile
+      val.next();
+      for (int n = 0; ok; ++n) {
+        if (!tc::warp_wait_fast(&item_full[n % kItems], ring_parity(n, kItems), abort_flag)) { ok = false; break; }
+        Item it = items[n % kItems];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&item_empty[n % kItems]);
+        it.len = __shfl_sync(0xFFFFFFFFu, it.len, 0);
+        it.qt = __shfl_sync(0xFFFFFFFFu, it.qt, 0);
+        if (it.len == 0) break;
+        const Work w(a, it);
+        // S_j of stream i; the stream that uses K_j (and Q) last releases it
+        auto issue_s = [&](int i, int j) -> bool {
+          const int st = key[i].slot;
+          if (!tc::warp_wait_fast(&full[st], key[i].phase, abort_flag)) return false;
+          tc::tc_fence_after();
+          key[i].next();
+          key[i].next();
+          const int keys = min(kM, w.keys[i] - j * kM);
+          const uint32_t id = tc::idesc_bf16_f32(kM, (keys + 15) / 16 * 16);
+          const uint32_t qa = tc::desc_k128_lo(sm0 + SM::kQ + i * SM::kQTile);
+          const uint32_t ka = tc::desc_k128_lo(sm0 + SM::kKV + st * SM::kStage + (SPLIT ? (uint32_t)i * kBox : 0u));
+          if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t kk = (uint32_t)(k & 3) * 32u;
-          tc::mma_bf16(tS, tc::smem_desc_k128(qa + (uint32_t)(k >> 2) * kQBox + kk),
-                       tc::smem_desc_k128(ka + (uint32_t)(k >> 2) * kKBox + kk), idS, k > 0 ? 1u : 0u);
+            for (int k = 0; k < HD / 16; ++k) {
+              const uint32_t off = ((uint32_t)(k >> 2) * kBox + (uint32_t)(k & 3) * 32u) >> 4;
+              tc::mma_bf16_lo(tm0 + (uint32_t)(kM * i), qa + off, ka + off, id, k > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(&s_full[i]);
+            if (i == (w.tiles[1] > j ? 1 : 0)) {
+              tc::mma_commit(&empty[st]);
+              if (j == w.most - 1) tc::mma_commit(q_empty);
+            }
+          }
+          __syncwarp();
+          return true;
+        };
+        ok = tc::warp_wait_fast(q_full, (uint32_t)n & 1u, abort_flag) && issue_s(0, 0) && (!w.tiles[1] || issue_s(1, 0));
+        for (int j = 0; ok && j < w.most; ++j) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= w.tiles[i]) continue;
+            // O += P_j V_j once the softmax has written P_j (in place of S_j) and V_j has landed
+            const int st = val.slot;
+            ok = tc::warp_wait_fast(&p_full[i], done[i] & 1u, abort_flag) &&
+                 tc::warp_wait_fast(&full[st], val.phase, abort_flag);
+            if (ok && j == 0) ok = tc::warp_wait_fast(&o_free[i], (outs[i] & 1u) ^ 1u, abort_flag);
+            if (!ok) break;
+            tc::tc_fence_after();
+            constexpr uint32_t idO = tc::idesc_bf16_f32(kM, HD) | (1u << 16);  // B (V) MN-major
+            const uint32_t va =
+                tc::desc_mn128_lo(sm0 + SM::kKV + st * SM::kStage + (SPLIT ? (uint32_t)i * kBox : 0u), kBox);
+            const uint32_t tO = tm0 + 2u * kM + (uint32_t)(HD * i), tP = tm0 + (uint32_t)(kM * i);
+            const int steps = (min(kM, w.keys[i] - j * kM) + 15) / 16;  // keys behind are not multiplied
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kM / 16; ++k)
+                if (k < steps)
+                  tc::mma_bf16_tmem_a_lo(tO, tP + 8u * k, va + (uint32_t)k * (2048u >> 4), idO,
+                                         (j > 0 || k > 0) ? 1u : 0u);
+              tc::mma_commit(&pv_done[i]);
+              if (i == (w.tiles[1] > j ? 1 : 0)) tc::mma_commit(&empty[st]);
+            }
+            __syncwarp();
+            // S_{j+1} replaces P_j, which the product must have read
+            ok = tc::warp_wait_fast(&pv_done[i], done[i] & 1u, abort_flag);
+            ++done[i];
+            if (ok && j + 1 < w.tiles[i]) ok = issue_s(i, j + 1);
+          }
+          val.next();
+          val.next();
         }
-        tc::mma_commit(&s_full[j & 1]);
-        tc::mma_commit(&k_empty[j % KS]);
-        return true;
-      };
-      bool ok = tc::mbar_wait(q_full, 0) && issue_s(0) && (n_kt < 2 || issue_s(1));
-      for (int j = 0; ok && j < n_kt; ++j) {
-        // O += P_j V_j once the softmax has written P_j (in place of S_j) and V_j has landed
-        ok = tc::mbar_wait(&p_full[j & 1], ring_parity(j, 2)) &&
-             tc::mbar_wait(&v_full[j % VS], ring_parity(j, VS));
-        if (!ok) break;
-        tc::tc_fence_after();
-        const uint32_t va = tc::smem_addr(sm + SM::kV + (j % VS) * SM::kKTile);
-        const uint32_t tP = tmem + (uint32_t)((j & 1) * kTBN);
+        // a stream that took fewer tiles goes on behind the item's last
 #pragma unroll
-        for (int k = 0; k < kTBN / 16; ++k) {
-          if (j * kTBN + 16 * k >= S) break;  // keys behind the sequence: not multiplied
-          const uint32_t boff = (uint32_t)k * 16u * 128u;  // 16 keys of 128-byte V rows
-          tc::mma_bf16_tmem_a(tO, tP + 8u * k, tc::smem_desc_mn128(va + boff, kKBox), idO,
-                              (j > 0 || k > 0) ? 1u : 0u);
-        }
-        tc::mma_commit(&pv_done[j & 1]);
-        tc::mma_commit(&v_empty[j % VS]);
-        if (j + 2 < n_kt) {
-          // S_{j+2} reuses buffer j % 2: wait until P_j V_j has read it
-          ok = tc::mbar_wait(&pv_done[j & 1], ring_parity(j, 2)) && issue_s(j + 2);
-        }
-      }
-      if (!ok) {
-        atomicOr(a.err, ZO_FLAG_TIMEOUT);
-        *abort_flag = 1;
-      }
-      tc::mma_commit(mma_done);  // arrives once every MMA issued above has retired
-    }
-  } else {  // softmax warps: TMEM lane quadrant qd holds the tile's query rows 32 qd .. +31
-    const int qd = warp & 3;
-    const int tr = 32 * qd + lane;  // row within the tile
-    const int r = q_first + tr;     // query position in the sequence
-    const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
-    float m_used = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < n_kt; ++j) {
-      const uint32_t tS = tmem + (uint32_t)((j & 1) * kTBN) + lane_off;
-      if (!warp_wait(&s_full[j & 1], ring_parity(j, 2), abort_flag)) { ok = false; break; }
-      tc::tc_fence_after();
-      float s[kTBN];
-#pragma unroll
-      for (int c = 0; c < kTBN / 32; ++c) tc::tmem_ld32(tS + 32u * c, s + 32 * c);
-      const int key0 = j * kTBN;
-      // the causal / sequence-end mask touches only the tiles that reach the diagonal or the
-      // end (uniform across the CTA: a real branch, not per-element selects)
-      if (key0 + kTBN - 1 > q_first || key0 + kTBN > S) {
-#pragma unroll
-        for (int c = 0; c < kTBN; ++c)
-          if (key0 + c > r || key0 + c >= S) s[c] = -INFINITY;
-      }
-      // the maximum of the raw scores (the scale is positive), then 2^(s * scale - m) with the
-      // scaling folded into the exponent's fused multiply-add
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // 4 independent chains
-#pragma unroll
-      for (int c = 0; c < kTBN; c += 2) mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], s[c], s[c + 1]);
-      const float mx = max3f(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-      const float m_new = fmaxf(m_used, mx);
-      // Lazy rescaling: keep the running maximum unless it grows by more than 2^8 (then
-      // O and l are rescaled, once the previous tile's P V has completed).
-      const bool need = j > 0 && m_new > m_used + 8.f;
-      const float m_old = m_used;
-      if (j == 0 || need) m_used = m_new;
-      const float msc = m_used == -INFINITY ? 0.f : m_used;
-      uint32_t pk[kTBN / 2];
-      float ls4[4] = {0.f, 0.f, 0.f, 0.f};  // two packed pairs of partial sums
-#pragma unroll
-      for (int c = 0; c < kTBN; c += 2) {
-        float x0, x1;
-        fma2_bc(s[c], s[c + 1], a.scale_log2, -msc, x0, x1);
-        const float p0 = ex2(x0), p1 = ex2(x1);
-        if ((c >> 1) & 1) add2(ls4[2], ls4[3], p0, p1);
-        else add2(ls4[0], ls4[1], p0, p1);
-        pk[c / 2] = pack_bf16x2(p0, p1);
-      }
-      const float lsum = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
-      if (__any_sync(0xFFFFFFFFu, need)) {
-        // O holds P_{j-1} V_{j-1} only once that MMA has completed
-        if (!warp_wait(&pv_done[(j - 1) & 1], ring_parity(j - 1, 2), abort_flag)) { ok = false; break; }
-        tc::tc_fence_after();
-        const float f = need ? ex2(m_old - m_new) : 1.f;
-        l *= f;
-#pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-          float o[32];
-          tc::tmem_ld32(tO + lane_off + 32u * c, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= f;
-          tc::tmem_st32(tO + lane_off + 32u * c, o);
-        }
-      }
-      // P_j overwrites the first kTBN / 2 columns of S_j (already read into registers)
-      tc::tmem_st32u(tS, pk);
-      l += lsum;
-      if (key0 + kTBN > S) {
-        // The rows behind the sequence (another one's, or padding) must not reach P V even with
-        // probability 0: 0 * NaN is NaN.  Thread t clears row t of the value tile.
-        if (!warp_wait(&v_full[j % VS], ring_parity(j, VS), abort_flag)) { ok = false; break; }
-        if (tr < kTBN && key0 + tr >= S) {
-          uint8_t *vrow = sm + SM::kV + (j % VS) * SM::kKTile + tr * 128;
-#pragma unroll
-          for (int c = 0; c < HD / 64; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4 *>(vrow + c * kKBox + 16 * i) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_proxy_async_smem();
-      }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&p_full[j & 1]);
-    }
-    if (ok && !warp_wait(&pv_done[(n_kt - 1) & 1], ring_parity(n_kt - 1, 2), abort_flag)) ok = false;
-    if (ok) {
-      tc::tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      uint16_t *orow = a.out + (int64_t)(row0 + r) * a.ldo + h * HD;
-      float worst = 0.f;  // NaN if any output of the row is not finite
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        float o[32];
-        tc::tmem_ld32(tO + lane_off + 32u * c, o);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          o[i] *= inv;
-          worst = fmaf(o[i], 0.f, worst);
-        }
-        if (r < S) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 w = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]),
-                                       pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                                       pack_bf16x2(o[8 * q + 4], o[8 * q + 5]),
-                                       pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
-            *reinterpret_cast<uint4 *>(orow + 32 * c + 8 * q) = w;
+        for (int i = 0; i < 2; ++i) {
+          outs[i] += w.tiles[i] != 0;
+          for (int j = w.tiles[i]; j < w.most; ++j) {
+            key[i].next();
+            key[i].next();
           }
         }
       }
-      const uint32_t suspects = __ballot_sync(0xFFFFFFFFu, r < S && worst != worst);
+      if (!ok && lane == 0) give_up();
       __syncwarp();
-      if (suspects) repair_rows<HD>(a, tile, q_first + 32 * qd, suspects, h, kvh, n_kt * kTBN);
-    } else if (lane == 0) {
-      atomicOr(a.err, ZO_FLAG_TIMEOUT);
-      *abort_flag = 1;
+      if (tc::elect_one()) tc::mma_commit(mma_done);  // arrives once every MMA issued above has retired
+    } else if (warp == 2) {  // items
+      Schedule sched(a);
+      for (int n = 0;; ++n) {
+        const int64_t c = n & 1 ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
+        const Item it = sched.at((int64_t)n * gridDim.x + c);
+        if (!tc::warp_wait_fast(&item_empty[n % kItems], ring_parity(n, kItems) ^ 1u, abort_flag)) {
+          if (lane == 0) give_up();
+          break;
+        }
+        if (lane == 0) {
+          items[n % kItems] = it;
+          tc::mbar_arrive(&item_full[n % kItems]);  // (release: the item is visible)
+        }
+        if (it.len == 0) break;
+      }
     }
+  } else {  // softmax: TMEM lane quadrant qd holds the stream's query rows 32 qd .. +31
+    tc::regs_inc<kMany>();
+    const int i = (warp - 4) / 4, qd = warp & 3;
+    const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
+    const uint32_t tS = tmem + (uint32_t)(kM * i) + lane_off, tO = tmem + 2u * kM + (uint32_t)(HD * i) + lane_off;
+    uint32_t done = 0;  // tiles of the stream so far
+    int base = 0;       // key tiles of the items before
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!tc::warp_wait_fast(&item_full[n % kItems], ring_parity(n, kItems), abort_flag)) {
+        ok = false;
+        break;
+      }
+      const Item it = items[n % kItems];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&item_empty[n % kItems]);
+      if (it.len == 0) break;
+      const Work w(a, it);
+      const int q0 = i ? w.q[1] : w.q[0], tiles = i ? w.tiles[1] : w.tiles[0], head = i ? w.head[1] : w.head[0];
+      const int key_end = i ? w.keys[1] : w.keys[0];
+      const int at = 2 * (base + w.most - 1) + 1;  // the last value tile's place in the ring
+      base += w.most;
+      if (tiles == 0) continue;
+      const int r = q0 + 32 * qd + lane;                     // query position in the sequence
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = 0; j < tiles; ++j, ++done) {
+        if (!tc::warp_wait_fast(&s_full[i], done & 1u, abort_flag)) { ok = false; break; }
+        tc::tc_fence_after();
+        const int key0 = j * kM;
+        const int last = min(r, w.len - 1) - key0;                // the row's last key in the tile
+        // the causal / sequence-end mask touches only the tiles that reach the diagonal or the end
+        if (key0 + kM - 1 <= min(q0 + 32 * qd, w.len - 1))
+          softmax_tile<HD, 4, false>(tS, tO, a.scale_log2, j == 0, last, m_used, l);
+        else if (key_end - key0 > 64)  // the keys that P V reads (uniform over the stream)
+          softmax_tile<HD, 4, true>(tS, tO, a.scale_log2, j == 0, last, m_used, l);
+        else if (key_end - key0 > 32)
+          softmax_tile<HD, 2, true>(tS, tO, a.scale_log2, j == 0, last, m_used, l);
+        else
+          softmax_tile<HD, 1, true>(tS, tO, a.scale_log2, j == 0, last, m_used, l);
+        if (j == w.most - 1 && w.ragged() && i == (w.tiles[0] == w.most ? 0 : 1)) {
+          // The value rows behind the sequence (another one's, or padding) in its last group of 16
+          // keys must not reach P V even with probability 0: 0 * NaN is NaN.  The stream whose
+          // product comes first clears them.
+          if (!tc::warp_wait_fast(&full[at % NS], ring_parity(at, NS), abort_flag)) { ok = false; break; }
+          const int first = w.len - key0, n = (16 - first % 16) * 8;  // n pieces of 16 bytes a box
+          uint8_t *tile = sm + SM::kKV + (at % NS) * SM::kStage + first * 128;
+          if (32 * qd + lane < n) {
+#pragma unroll
+            for (int c = 0; c < (int)(SM::kStage / kBox); ++c)
+              *reinterpret_cast<uint4 *>(tile + c * kBox + 16 * (32 * qd + lane)) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[i]);
+      }
+      if (!ok) break;
+      if (!tc::warp_wait_fast(&pv_done[i], (done - 1u) & 1u, abort_flag)) { ok = false; break; }
+      tc::tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      uint16_t *orow = a.out + (int64_t)(w.row0 + r) * a.ldo + (int64_t)head * HD;
+      float worst = 0.f;  // NaN if any output of the row is not finite
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        tc::tmem_ld32(tO + (uint32_t)c, o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          o[e] *= inv;
+          worst = fmaf(o[e], 0.f, worst);
+        }
+        if (r < w.len) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4 *>(orow + c + e) =
+                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&o_free[i]);
+      const uint32_t suspects = __ballot_sync(0xFFFFFFFFu, r < w.len && worst != worst);
+      __syncwarp();
+      if (suspects)
+        repair_rows<HD>(a, w.row0, w.len, q0 + 32 * qd, suspects, head, head / (a.H / a.Hk), tiles * kM);
+    }
+    if (!ok && lane == 0) give_up();
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -445,14 +604,17 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
 }
 
-template <int HD>
+template <int HD, bool SPLIT>
 zo_status launch(zo_ctx *ctx, const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                  const PackedArgs &a) {
-  using SM = PackedSmem<HD>;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(attn_packed_kernel<HD>), (int)SM::kBytes);
+  using SM = PackedSmem<HD, SPLIT>;
+  const auto kernel = attn_packed_kernel<HD, SPLIT>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), (int)SM::kBytes);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "attn_packed_kernel attribute: %s", cudaGetErrorString(e));
-  const dim3 grid((unsigned)((int64_t)(a.total + kTBM - 1) / kTBM + a.n_seqs), a.H);
-  attn_packed_kernel<HD><<<grid, kTThreads, SM::kBytes, ctx->stream>>>(tmq, tmk, tmv, a);
+  // at most this many items
+  const int64_t per = a.mode == kRows ? 2 * kM : kM, group = a.mode == kRows ? a.H : a.H / 2;
+  const int64_t items = (((int64_t)a.total + per - 1) / per + a.n_seqs) * group;
+  kernel<<<(unsigned)(items < kSmCount ? items : kSmCount), kThreads, SM::kBytes, ctx->stream>>>(tmq, tmk, tmv, a);
   return check_launch(ctx, "attn_packed_kernel");
 }
 
@@ -486,14 +648,15 @@ extern "C" zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void 
   if (device.status != cudaSuccess)
     return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
   CUtensorMap tmq, tmk, tmv;
-  constexpr int kBN = PackedCfg<128>::kBN;  // the same for both head dims
-  if (!tile_map_bf16(&tmq, q, total_tokens, wq, ldq, kTBM) ||
-      !tile_map_bf16(&tmk, k, total_tokens, wk, ldk, kBN) ||
-      !tile_map_bf16(&tmv, v, total_tokens, wk, ldv, kBN))
+  if (!tile_map_bf16(&tmq, q, total_tokens, wq, ldq, kM) || !tile_map_bf16(&tmk, k, total_tokens, wk, ldk, kM) ||
+      !tile_map_bf16(&tmv, v, total_tokens, wk, ldv, kM))
     return fail(ctx, ZO_ERR_CUDA, "attention_packed: cuTensorMapEncodeTiled failed");
+  const int shared = n_heads / n_kv_heads;
+  const Mode mode = shared % 2 == 0 ? kHeads : head_dim == 64 && shared == 1 && n_heads % 2 == 0 ? kPair64 : kRows;
   const PackedArgs a{static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
                      static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out), cu_seqlens, n_seqs,
                      (int)total_tokens, n_heads, n_kv_heads, ldq, ldk, ldv, ldo,
-                     scale * 1.4426950408889634f, &ctx->dstate->flags};
-  return head_dim == 64 ? launch<64>(ctx, tmq, tmk, tmv, a) : launch<128>(ctx, tmq, tmk, tmv, a);
+                     scale * 1.4426950408889634f, (int)mode, &ctx->dstate->flags};
+  if (head_dim == 128) return launch<128, false>(ctx, tmq, tmk, tmv, a);
+  return mode == kPair64 ? launch<64, true>(ctx, tmq, tmk, tmv, a) : launch<64, false>(ctx, tmq, tmk, tmv, a);
 }
