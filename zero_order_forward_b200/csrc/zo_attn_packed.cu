@@ -39,7 +39,7 @@ using tc::fma2_bc;
 using tc::max3f;
 using tc::ring_parity;
 
-constexpr int kM = 128;                // query rows of a stream, keys of a tile
+constexpr int kM = 128;                // query rows of a stream, keys of a tile (2^7: Schedule)
 constexpr int kWarps = 12;             // loads, MMAs, items, an idle one; 2 x 4 softmax
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kBox = kM * 128;    // bytes of one 128-row x 64-column bf16 box
@@ -101,30 +101,32 @@ struct Work {
   __device__ __forceinline__ bool ragged() const { return most * kM >= len && len % 16 != 0; }
 };
 
-// Tiles of `per` rows of sequence i; 0 if it is empty or its offsets decrease or leave [0, total].
-__device__ __forceinline__ int seq_tiles(const PackedArgs &a, int i, int per, bool &bad) {
+// Tiles of 2^shift rows of sequence i; 0 if it is empty or its offsets decrease or leave [0, total].
+__device__ __forceinline__ int seq_tiles(const PackedArgs &a, int i, int shift, bool &bad) {
   bad = false;
   if (i >= a.n_seqs) return 0;
   const int s = __ldg(a.cu + i), e = __ldg(a.cu + i + 1);
   bad = s < 0 || e < s || e > a.total;
-  return bad ? 0 : (int)(((int64_t)e - s + per - 1) / per);
+  return bad ? 0 : (int)(((uint32_t)(e - s) + (1u << shift) - 1u) >> shift);
 }
 
 // The items of one CTA in their order (one warp).
 struct Schedule {
   const PackedArgs &a;
-  int per, group;          // rows of a tile; items of one tile (heads, or pairs of them)
+  int shift, group;        // log2 of a tile's rows; items of one tile (heads, or pairs of them)
   int lane, first_tiles;   // this lane's count of the first 32 sequences
   int level, count;        // sequences with more than `level` tiles: `count`
   int64_t base;            // items of the longer levels
+  int from, before;        // sequences [0, from) have `before` of the level's
   __device__ __forceinline__ Schedule(const PackedArgs &args) : a(args) {
     lane = threadIdx.x & 31;
-    per = a.mode == kRows ? 2 * kM : kM;
+    shift = a.mode == kRows ? 8 : 7;
+    from = before = 0;
     group = a.mode == kRows ? a.H : a.H / 2;
     int most = 0, any_bad = 0;
     for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
       bool bad;
-      const int n = seq_tiles(a, i0 + lane, per, bad);
+      const int n = seq_tiles(a, i0 + lane, shift, bad);
       if (i0 == 0) first_tiles = n;
       most = max(most, n);
       any_bad |= bad;
@@ -136,7 +138,7 @@ struct Schedule {
   }
   __device__ __forceinline__ bool has(int i0) const {
     bool bad;
-    return (i0 == 0 ? first_tiles : seq_tiles(a, i0 + lane, per, bad)) > level;
+    return (i0 == 0 ? first_tiles : seq_tiles(a, i0 + lane, shift, bad)) > level;
   }
   __device__ __forceinline__ int sequences() const {
     int n = 0;
@@ -148,25 +150,25 @@ struct Schedule {
     while (level >= 0 && slot >= base + (int64_t)count * group) {
       base += (int64_t)count * group;
       --level;
+      from = before = 0;
       if (level >= 0) count = sequences();
     }
     Item it{0, 0, 0, 0};
     if (level < 0) return it;
     const int index = (int)(slot - base);
-    int nth = index / group;
-    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
-      const uint32_t in = __ballot_sync(0xFFFFFFFFu, has(i0));
-      const int n = __popc(in);
-      if (nth < n) {
+    const int nth = index / group;
+    for (; from < a.n_seqs; from += 32) {
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, has(from));
+      if (nth < before + __popc(in)) {
         const uint32_t lower = in & ((1u << lane) - 1u);
-        const int i = i0 + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && __popc(lower) == nth)) - 1;
+        const int i = from + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && before + __popc(lower) == nth)) - 1;
         it.row0 = __ldg(a.cu + i);
         it.len = __ldg(a.cu + i + 1) - it.row0;
         it.qt = level;
-        it.head = (index - index / group * group) * (a.mode == kRows ? 1 : 2);
+        it.head = (index - nth * group) * (a.mode == kRows ? 1 : 2);
         break;
       }
-      nth -= n;
+      before += __popc(in);
     }
     return it;
   }
@@ -287,7 +289,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
     for (int e = 0; e < 32; e += 2) {
       float x0, x1;
       fma2_bc(s[32 * c + e], s[32 * c + e + 1], scale_log2, -msc, x0, x1);
-      const float p0 = ex2(x0), p1 = ex2(x1);
+      float p0, p1;
+      if (!MASK && (e >> 1) % 4 == 3) {  // a quarter beside the special-function unit
+        tc::ex2_poly2(x0, x1, p0, p1);
+      } else {
+        p0 = ex2(x0);
+        p1 = ex2(x1);
+      }
       if ((e >> 1) & 1) add2(ls4[2], ls4[3], p0, p1);
       else add2(ls4[0], ls4[1], p0, p1);
       pk[e / 2] = pack_bf16x2(p0, p1);
@@ -414,10 +422,13 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         it.qt = __shfl_sync(0xFFFFFFFFu, it.qt, 0);
         if (it.len == 0) break;
         const Work w(a, it);
+        // K_j is there (it is for the second stream if the first has used it)
+        auto wait_k = [&](int i, int j) -> bool {
+          return (i == 1 && j < w.tiles[0]) || tc::warp_wait_fast(&full[key[i].slot], key[i].phase, abort_flag);
+        };
         // S_j of stream i; the stream that uses K_j (and Q) last releases it
-        auto issue_s = [&](int i, int j) -> bool {
+        auto issue_s = [&](int i, int j) {
           const int st = key[i].slot;
-          if (!tc::warp_wait_fast(&full[st], key[i].phase, abort_flag)) return false;
           tc::tc_fence_after();
           key[i].next();
           key[i].next();
@@ -438,17 +449,21 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             }
           }
           __syncwarp();
-          return true;
         };
-        ok = tc::warp_wait_fast(q_full, (uint32_t)n & 1u, abort_flag) && issue_s(0, 0) && (!w.tiles[1] || issue_s(1, 0));
+        ok = tc::warp_wait_fast(q_full, (uint32_t)n & 1u, abort_flag) && wait_k(0, 0);
+        if (ok) {
+          issue_s(0, 0);
+          if (w.tiles[1]) issue_s(1, 0);
+        }
         for (int j = 0; ok && j < w.most; ++j) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!ok || j >= w.tiles[i]) continue;
             // O += P_j V_j once the softmax has written P_j (in place of S_j) and V_j has landed
             const int st = val.slot;
-            ok = tc::warp_wait_fast(&p_full[i], done[i] & 1u, abort_flag) &&
-                 tc::warp_wait_fast(&full[st], val.phase, abort_flag);
+            // (tiles that the other stream has seen land need no second look)
+            if (i == 0 || j >= w.tiles[0]) ok = tc::warp_wait_fast(&full[st], val.phase, abort_flag);
+            ok = ok && tc::warp_wait_fast(&p_full[i], done[i] & 1u, abort_flag);
             if (ok && j == 0) ok = tc::warp_wait_fast(&o_free[i], (outs[i] & 1u) ^ 1u, abort_flag);
             if (!ok) break;
             tc::tc_fence_after();
@@ -468,9 +483,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             }
             __syncwarp();
             // S_{j+1} replaces P_j, which the product must have read
-            ok = tc::warp_wait_fast(&pv_done[i], done[i] & 1u, abort_flag);
+            if (j + 1 < w.tiles[i]) ok = wait_k(i, j + 1);
+            ok = ok && tc::warp_wait_fast(&pv_done[i], done[i] & 1u, abort_flag);
             ++done[i];
-            if (ok && j + 1 < w.tiles[i]) ok = issue_s(i, j + 1);
+            if (ok && j + 1 < w.tiles[i]) issue_s(i, j + 1);
           }
           val.next();
           val.next();
