@@ -57,7 +57,7 @@ struct PackedSmem {
   static constexpr uint32_t kBar = kKV + kStages * kStage;
   static constexpr int kNumBars = 2 * kStages + 2 + 8 + 2 * kItems + 1;
   static constexpr uint32_t kItem = kBar + 8 * ((kNumBars + 2) / 2 * 2);   // Item [kItems]
-  static constexpr uint32_t kBytes = kItem + kItems * 32 + 1024;           // + alignment slack
+  static constexpr uint32_t kBytes = kItem + kItems * 48 + 1024;           // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -72,34 +72,37 @@ struct PackedArgs {
   uint32_t *err;
 };
 
-struct Item {
-  int row0, len;   // the sequence's first row and length (0: no more items)
-  int qt;          // tile of the item (of 128 rows, or 256: kRows) within the sequence
-  int head;        // stream 0's query head
-};
-
-// What the streams of an item do, from the item.
-struct Work {
-  int row0, len, kvh;
-  int q[2], head[2], keys[2], tiles[2];  // first query row, head, keys and key tiles (0: no such stream)
-  int most;                              // key tiles of the longer stream
-  __device__ __forceinline__ Work(const PackedArgs &a, const Item &it) {
-    row0 = it.row0;
-    len = it.len;
-    const bool rows = a.mode == kRows;
-    kvh = it.head / (a.H / a.Hk);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      q[i] = rows ? 2 * kM * it.qt + kM * i : kM * it.qt;
-      head[i] = rows ? it.head : it.head + i;
-      keys[i] = q[i] < len ? min(q[i] + kM, len) : 0;
-      tiles[i] = (keys[i] + kM - 1) / kM;
-    }
-    most = max(tiles[0], tiles[1]);
-  }
+// What the two streams of an item do.
+struct alignas(16) Item {
+  int row0, len;  // the sequence's first row and length (0: no more items)
+  int kvh;        // key/value head (of stream 0)
+  int most;       // key tiles of the longer stream
+  int q[2];       // first query row
+  int head[2];    // query head
+  int keys[2];    // keys of the stream's tile (0: no such stream)
+  int tiles[2];   // key tiles
   // The last tile's value rows behind the sequence share a group of 16 with its own.
   __device__ __forceinline__ bool ragged() const { return most * kM >= len && len % 16 != 0; }
 };
+
+// Item of tile `qt` (of 128 rows, or 256: kRows) of a sequence and its heads' number `h`.
+__device__ __forceinline__ Item make_item(const PackedArgs &a, int row0, int len, int qt, int h) {
+  const bool rows = a.mode == kRows;
+  Item it;
+  it.row0 = row0;
+  it.len = len;
+  it.most = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    it.q[i] = rows ? 2 * kM * qt + kM * i : kM * qt;
+    it.head[i] = rows ? h : 2 * h + i;
+    it.keys[i] = it.q[i] < len ? min(it.q[i] + kM, len) : 0;
+    it.tiles[i] = (it.keys[i] + kM - 1) / kM;
+    it.most = max(it.most, it.tiles[i]);
+  }
+  it.kvh = it.head[0] / (a.H / a.Hk);
+  return it;
+}
 
 // Tiles of 2^shift rows of sequence i; 0 if it is empty or its offsets decrease or leave [0, total].
 __device__ __forceinline__ int seq_tiles(const PackedArgs &a, int i, int shift, bool &bad) {
@@ -116,7 +119,7 @@ struct Schedule {
   int shift, group;        // log2 of a tile's rows; items of one tile (heads, or pairs of them)
   int lane, first_tiles;   // this lane's count of the first 32 sequences
   int level, count;        // sequences with more than `level` tiles: `count`
-  int64_t base;            // items of the longer levels
+  int64_t base, total;     // items of the longer levels; of all
   int from, before;        // sequences [0, from) have `before` of the level's
   __device__ __forceinline__ Schedule(const PackedArgs &args) : a(args) {
     lane = threadIdx.x & 31;
@@ -124,14 +127,19 @@ struct Schedule {
     from = before = 0;
     group = a.mode == kRows ? a.H : a.H / 2;
     int most = 0, any_bad = 0;
+    int64_t tiles = 0;
     for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
       bool bad;
       const int n = seq_tiles(a, i0 + lane, shift, bad);
       if (i0 == 0) first_tiles = n;
       most = max(most, n);
+      tiles += n;
       any_bad |= bad;
     }
     if (blockIdx.x == 0 && any_bad) atomicOr(a.err, ZO_FLAG_OFFSETS);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, o);
+    total = tiles * group;
     level = __reduce_max_sync(0xFFFFFFFFu, most) - 1;
     base = 0;
     count = level >= 0 ? sequences() : 0;
@@ -153,7 +161,7 @@ struct Schedule {
       from = before = 0;
       if (level >= 0) count = sequences();
     }
-    Item it{0, 0, 0, 0};
+    Item it{};
     if (level < 0) return it;
     const int index = (int)(slot - base);
     const int nth = index / group;
@@ -162,10 +170,8 @@ struct Schedule {
       if (nth < before + __popc(in)) {
         const uint32_t lower = in & ((1u << lane) - 1u);
         const int i = from + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && before + __popc(lower) == nth)) - 1;
-        it.row0 = __ldg(a.cu + i);
-        it.len = __ldg(a.cu + i + 1) - it.row0;
-        it.qt = level;
-        it.head = (index - nth * group) * (a.mode == kRows ? 1 : 2);
+        const int row0 = __ldg(a.cu + i);
+        it = make_item(a, row0, __ldg(a.cu + i + 1) - row0, level, index - nth * group);
         break;
       }
       before += __popc(in);
@@ -306,6 +312,23 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
   tc::tmem_st_wait();
 }
 
+// The words a[0 .. 3] of a quad's lanes transposed: a[k] becomes lane k's word of this lane's number.
+__device__ __forceinline__ void quad_transpose(uint32_t (&a)[4]) {
+  const int c = threadIdx.x & 3;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, c & 1 ? a[k] : a[k + 1], 1);
+    if (c & 1) a[k] = v;
+    else a[k + 1] = v;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, c & 2 ? a[k] : a[k + 2], 2);
+    if (c & 2) a[k] = v;
+    else a[k + 2] = v;
+  }
+}
+
 template <int HD, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -382,10 +405,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         bool ok = true;
         int n_q = 0;
         for (int n = 0; ok; ++n) {
-          Item it;
-          ok = next_item(n, it);
-          if (!ok || it.len == 0) break;
-          const Work w(a, it);
+          Item w;
+          ok = next_item(n, w);
+          if (!ok || w.len == 0) break;
           ok = wait(q_empty, ((uint32_t)n & 1u) ^ 1u);
           if (!ok) break;
           n_q = n + 1;
@@ -415,13 +437,18 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       val.next();
       for (int n = 0; ok; ++n) {
         if (!tc::warp_wait_fast(&item_full[n % kItems], ring_parity(n, kItems), abort_flag)) { ok = false; break; }
-        Item it = items[n % kItems];
+        Item w = items[n % kItems];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&item_empty[n % kItems]);
-        it.len = __shfl_sync(0xFFFFFFFFu, it.len, 0);
-        it.qt = __shfl_sync(0xFFFFFFFFu, it.qt, 0);
-        if (it.len == 0) break;
-        const Work w(a, it);
+        // alike in all lanes, which the compiler is to know
+        w.len = __shfl_sync(0xFFFFFFFFu, w.len, 0);
+        w.most = __shfl_sync(0xFFFFFFFFu, w.most, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          w.keys[i] = __shfl_sync(0xFFFFFFFFu, w.keys[i], 0);
+          w.tiles[i] = __shfl_sync(0xFFFFFFFFu, w.tiles[i], 0);
+        }
+        if (w.len == 0) break;
         // K_j is there (it is for the second stream if the first has used it)
         auto wait_k = [&](int i, int j) -> bool {
           return (i == 1 && j < w.tiles[0]) || tc::warp_wait_fast(&full[key[i].slot], key[i].phase, abort_flag);
@@ -507,7 +534,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     } else if (warp == 2) {  // items
       Schedule sched(a);
       for (int n = 0;; ++n) {
-        const int64_t c = n & 1 ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
+        // to and fro; the last round, which has items for some CTAs only, for those with the least so far
+        const bool back = (n & 1) || (n > 0 && (int64_t)(n + 1) * gridDim.x >= sched.total);
+        const int64_t c = back ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
         const Item it = sched.at((int64_t)n * gridDim.x + c);
         if (!tc::warp_wait_fast(&item_empty[n % kItems], ring_parity(n, kItems) ^ 1u, abort_flag)) {
           if (lane == 0) give_up();
@@ -533,17 +562,17 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         ok = false;
         break;
       }
-      const Item it = items[n % kItems];
+      const Item w = items[n % kItems];
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&item_empty[n % kItems]);
-      if (it.len == 0) break;
-      const Work w(a, it);
+      if (w.len == 0) break;
       const int q0 = i ? w.q[1] : w.q[0], tiles = i ? w.tiles[1] : w.tiles[0], head = i ? w.head[1] : w.head[0];
       const int key_end = i ? w.keys[1] : w.keys[0];
       const int at = 2 * (base + w.most - 1) + 1;  // the last value tile's place in the ring
       base += w.most;
       if (tiles == 0) continue;
       const int r = q0 + 32 * qd + lane;                     // query position in the sequence
+      const bool any = q0 + 32 * qd < w.len;                 // this warp has a row
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < tiles; ++j, ++done) {
         if (!tc::warp_wait_fast(&s_full[i], done & 1u, abort_flag)) { ok = false; break; }
@@ -551,7 +580,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         const int key0 = j * kM;
         const int last = min(r, w.len - 1) - key0;                // the row's last key in the tile
         // the causal / sequence-end mask touches only the tiles that reach the diagonal or the end
-        if (key0 + kM - 1 <= min(q0 + 32 * qd, w.len - 1))
+        if (!any) {
+          // rows behind the sequence: whatever P holds, their outputs are not read
+        } else if (key0 + kM - 1 <= min(q0 + 32 * qd, w.len - 1))
           softmax_tile<HD, 4, false>(tS, tO, a.scale_log2, j == 0, last, m_used, l);
         else if (key_end - key0 > 64)  // the keys that P V reads (uniform over the stream)
           softmax_tile<HD, 4, true>(tS, tO, a.scale_log2, j == 0, last, m_used, l);
@@ -581,10 +612,11 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       if (!tc::warp_wait_fast(&pv_done[i], (done - 1u) & 1u, abort_flag)) { ok = false; break; }
       tc::tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      uint16_t *orow = a.out + (int64_t)(w.row0 + r) * a.ldo + (int64_t)head * HD;
+      const int r_quad = r - lane % 4;
+      uint16_t *orow = a.out + (int64_t)(w.row0 + r_quad) * a.ldo + (int64_t)head * HD + 8 * (lane % 4);
       float worst = 0.f;  // NaN if any output of the row is not finite
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 32) {
+      for (int c = 0; any && c < HD; c += 32) {
         float o[32];
         tc::tmem_ld32(tO + (uint32_t)c, o);
 #pragma unroll
@@ -592,13 +624,19 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
           o[e] *= inv;
           worst = fmaf(o[e], 0.f, worst);
         }
-        if (r < w.len) {
+        // the quad's 4 rows x 4 pieces of 16 bytes transposed: a store takes 64 bytes of 8 rows, not 16
+        // bytes of 32 rows
+        uint32_t v[4][4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4 *>(orow + c + e) =
-                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[e][k] = pack_bf16x2(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
+          quad_transpose(v[e]);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (r_quad + k < w.len)
+            *reinterpret_cast<uint4 *>(orow + k * a.ldo + c) = make_uint4(v[0][k], v[1][k], v[2][k], v[3][k]);
       }
       tc::tc_fence_before();
       __syncwarp();
