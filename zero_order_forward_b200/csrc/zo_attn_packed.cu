@@ -68,7 +68,7 @@ struct PackedArgs {
   int n_seqs, total, H, Hk;
   int64_t ldq, ldk, ldv, ldo;
   float scale_log2;
-  int mode;
+  int mode, shared;  // query heads of a key/value head
   uint32_t *err;
 };
 
@@ -100,7 +100,7 @@ __device__ __forceinline__ Item make_item(const PackedArgs &a, int row0, int len
     it.tiles[i] = (it.keys[i] + kM - 1) / kM;
     it.most = max(it.most, it.tiles[i]);
   }
-  it.kvh = it.head[0] / (a.H / a.Hk);
+  it.kvh = it.head[0] / a.shared;
   return it;
 }
 
@@ -117,7 +117,8 @@ __device__ __forceinline__ int seq_tiles(const PackedArgs &a, int i, int shift, 
 struct Schedule {
   const PackedArgs &a;
   int shift, group;        // log2 of a tile's rows; items of one tile (heads, or pairs of them)
-  int lane, first_tiles;   // this lane's count of the first 32 sequences
+  int lane, first_tiles;   // this lane's count of the first 32 sequences, their rows
+  int first_row, first_len;
   int level, count;        // sequences with more than `level` tiles: `count`
   int64_t base, total;     // items of the longer levels; of all
   int from, before;        // sequences [0, from) have `before` of the level's
@@ -126,6 +127,8 @@ struct Schedule {
     shift = a.mode == kRows ? 8 : 7;
     from = before = 0;
     group = a.mode == kRows ? a.H : a.H / 2;
+    first_row = lane < a.n_seqs ? __ldg(a.cu + lane) : 0;
+    first_len = lane < a.n_seqs ? __ldg(a.cu + lane + 1) - first_row : 0;
     int most = 0, any_bad = 0;
     int64_t tiles = 0;
     for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
@@ -170,8 +173,12 @@ struct Schedule {
       if (nth < before + __popc(in)) {
         const uint32_t lower = in & ((1u << lane) - 1u);
         const int i = from + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && before + __popc(lower) == nth)) - 1;
-        const int row0 = __ldg(a.cu + i);
-        it = make_item(a, row0, __ldg(a.cu + i + 1) - row0, level, index - nth * group);
+        int row0 = __shfl_sync(0xFFFFFFFFu, first_row, i & 31), len = __shfl_sync(0xFFFFFFFFu, first_len, i & 31);
+        if (from > 0) {
+          row0 = __ldg(a.cu + i);
+          len = __ldg(a.cu + i + 1) - row0;
+        }
+        it = make_item(a, row0, len, level, index - nth * group);
         break;
       }
       before += __popc(in);
@@ -258,9 +265,15 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
 #pragma unroll
   for (int c = 0; c < NC; ++c) tc::tmem_ld_seal(s + 32 * c);
   if (MASK) {
+    // (of a tile on the diagonal, a warp's rows have one group of 32 keys that is neither in nor out)
 #pragma unroll
-    for (int e = 0; e < 32 * NC; ++e)
-      if (e > last) s[e] = -INFINITY;
+    for (int c = 0; c < NC; ++c) {
+      if (__any_sync(0xFFFFFFFFu, last < 32 * c + 31)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (32 * c + e > last) s[32 * c + e] = -INFINITY;
+      }
+    }
   }
   // the maximum of the raw scores (the scale is positive), then 2^(s * scale - m) with the
   // scaling folded into the exponent's fused multiply-add
@@ -295,13 +308,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
     for (int e = 0; e < 32; e += 2) {
       float x0, x1;
       fma2_bc(s[32 * c + e], s[32 * c + e + 1], scale_log2, -msc, x0, x1);
-      float p0, p1;
-      if (!MASK && (e >> 1) % 4 == 3) {  // a quarter beside the special-function unit
-        tc::ex2_poly2(x0, x1, p0, p1);
-      } else {
-        p0 = ex2(x0);
-        p1 = ex2(x1);
-      }
+      const float p0 = ex2(x0), p1 = ex2(x1);
       if ((e >> 1) & 1) add2(ls4[2], ls4[3], p0, p1);
       else add2(ls4[0], ls4[1], p0, p1);
       pk[e / 2] = pack_bf16x2(p0, p1);
@@ -614,25 +621,23 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int r_quad = r - lane % 4;
       uint16_t *orow = a.out + (int64_t)(w.row0 + r_quad) * a.ldo + (int64_t)head * HD + 8 * (lane % 4);
-      float worst = 0.f;  // NaN if any output of the row is not finite
+      uint32_t worst = 0;  // two bf16, NaN if any output of the row is not finite
 #pragma unroll 1
       for (int c = 0; any && c < HD; c += 32) {
         float o[32];
         tc::tmem_ld32(tO + (uint32_t)c, o);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          o[e] *= inv;
-          worst = fmaf(o[e], 0.f, worst);
-        }
         // the quad's 4 rows x 4 pieces of 16 bytes transposed: a store takes 64 bytes of 8 rows, not 16
         // bytes of 32 rows
         uint32_t v[4][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[e][k] = pack_bf16x2(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
-          quad_transpose(v[e]);
-        }
+          for (int k = 0; k < 4; ++k) {
+            v[e][k] = pack_bf16x2(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+            worst = tc::zero_or_nan2(v[e][k], worst);
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) quad_transpose(v[e]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (r_quad + k < w.len)
@@ -641,10 +646,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&o_free[i]);
-      const uint32_t suspects = __ballot_sync(0xFFFFFFFFu, r < w.len && worst != worst);
+      const uint32_t suspects = __ballot_sync(0xFFFFFFFFu, r < w.len && worst != 0);
       __syncwarp();
       if (suspects)
-        repair_rows<HD>(a, w.row0, w.len, q0 + 32 * qd, suspects, head, head / (a.H / a.Hk), tiles * kM);
+        repair_rows<HD>(a, w.row0, w.len, q0 + 32 * qd, suspects, head, head / a.shared, tiles * kM);
     }
     if (!ok && lane == 0) give_up();
   }
@@ -663,13 +668,16 @@ zo_status launch(zo_ctx *ctx, const CUtensorMap &tmq, const CUtensorMap &tmk, co
                  const PackedArgs &a) {
   using SM = PackedSmem<HD, SPLIT>;
   const auto kernel = attn_packed_kernel<HD, SPLIT>;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), (int)SM::kBytes);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), (int)SM::kBytes);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "attn_packed_kernel attribute: %s", cudaGetErrorString(e));
   // at most this many items
   const int64_t per = a.mode == kRows ? 2 * kM : kM, group = a.mode == kRows ? a.H : a.H / 2;
   const int64_t items = (((int64_t)a.total + per - 1) / per + a.n_seqs) * group;
-  kernel<<<(unsigned)(items < kSmCount ? items : kSmCount), kThreads, SM::kBytes, ctx->stream>>>(tmq, tmk, tmv, a);
-  return check_launch(ctx, "attn_packed_kernel");
+  e = launch_early(kernel, dim3((unsigned)(items < kSmCount ? items : kSmCount)), kThreads, (int)SM::kBytes, ctx->stream,
+                   tmq, tmk, tmv, a);
+  if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "attn_packed_kernel: %s", cudaGetErrorString(e));
+  ctx->launches += 1;
+  return ZO_OK;
 }
 
 }  // namespace
@@ -710,7 +718,7 @@ extern "C" zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void 
   const PackedArgs a{static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
                      static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out), cu_seqlens, n_seqs,
                      (int)total_tokens, n_heads, n_kv_heads, ldq, ldk, ldv, ldo,
-                     scale * 1.4426950408889634f, (int)mode, &ctx->dstate->flags};
+                     scale * 1.4426950408889634f, (int)mode, shared, &ctx->dstate->flags};
   if (head_dim == 128) return launch<128, false>(ctx, tmq, tmk, tmv, a);
   return mode == kPair64 ? launch<64, true>(ctx, tmq, tmk, tmv, a) : launch<64, false>(ctx, tmq, tmk, tmv, a);
 }

@@ -188,6 +188,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  tc::pdl_wait();
 
   uint32_t issued = 0;
   if (warp == 0 && lane == 0) {
@@ -341,6 +342,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   tc::cluster_sync();  // both CTAs' barriers initialised and tensor memory allocated
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  tc::pdl_wait();
   const uint32_t full_leader = tc::map_to_rank(full, 0);
   const uint32_t acc_empty_leader = tc::map_to_rank(acc_empty, 0);
   const uint32_t abort_peer = tc::map_to_rank(const_cast<int *>(abort_flag), rank ^ 1u);
@@ -462,6 +464,7 @@ __global__ void __launch_bounds__(256)
 head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
   constexpr int N = (kSmCount + 31) / 32;  // triples of a lane (148 at most in all)
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  tc::pdl_launch_dependents();
   tc::pdl_wait();
   if (row >= a.rows) return;
   const float4 *part = a.part + (int64_t)row * a.splits;
@@ -609,19 +612,10 @@ zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_kernel attribute: %s", cudaGetErrorString(e));
   const int64_t m = (rows + kBM - 1) / kBM;
   const dim3 grid((unsigned)(pairs ? (m + 1) / 2 * 2 : m), (unsigned)a.splits);
-  kernel<<<grid, kThreads, smem, ctx->stream>>>(ta, tb, a);
-  zo_status st = check_launch(ctx, "head_kernel");
-  if (st != ZO_OK) return st;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = ctx->stream;
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, head_join_kernel, a, logprob, entropy);
+  e = launch_early(kernel, grid, kThreads, smem, ctx->stream, ta, tb, a);
+  if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_kernel: %s", cudaGetErrorString(e));
+  ctx->launches += 1;
+  e = launch_early(head_join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, ctx->stream, a, logprob, entropy);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_join_kernel: %s", cudaGetErrorString(e));
   ctx->launches += 1;
   return ZO_OK;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "zo.h"
@@ -238,6 +239,23 @@ void ktime_end(zo_ctx *ctx, int slot, int cls, double work);
 // zo_step's body for device-resident losses (what the step drivers call).
 zo_status step_device(zo_ctx *ctx, const double *loss_plus, const double *loss_minus, int32_t n_pert,
                       const double *loss0, float lr, float eps, float damping);
+
+// Launch that may start before the kernel ahead of it in the stream has ended (its blocks wait
+// for that end themselves: tc::pdl_wait, before they touch anything but their own memory).
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A &&...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 // Makes a context's device current for a call and puts the caller's back at its end.
 struct DeviceScope {

@@ -100,6 +100,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two bf16 sums: acc + 0 * v, which is NaN from the first infinity or NaN on and +-0 before.  From
+// acc = 0 the word stays 0 unless there is one (0 + -0 = 0).
+__device__ __forceinline__ uint32_t zero_or_nan2(uint32_t v, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(acc));
+  return d;
+}
+
 // max(a, b, c): one three-input instruction instead of two.
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
@@ -129,31 +137,6 @@ __device__ __forceinline__ void fma2(float &u0, float &u1, float a0, float a1, f
       "mov.b64 u, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
       "fma.rn.f32x2 u, a, b, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
       : "+f"(u0), "+f"(u1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
-// (2^x0, 2^x1) within 2^-18.5 relative for x >= -126 (below: 2^-126; NaN stays NaN), without the
-// special-function unit: x = n + f with n the nearest whole number, 2^f by a polynomial of degree 4 on
-// [-1/2, 1/2] (relative minimax fit), times 2^n made from n's bits.  Two elements per instruction
-// on the FMA pipe, which has time where that unit's 16 results a clock are the bound.
-__device__ __forceinline__ void ex2_poly2(float x0, float x1, float &p0, float &p1) {
-  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(x0) : "f"(x0));
-  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(x1) : "f"(x1));
-  constexpr float kMagic = 12582912.f + 127.f;  // 1.5 2^23: n + 127 in the low bits of x + kMagic
-  constexpr float c4 = 0.00957010034f, c3 = 0.0559178591f, c2 = 0.240247443f, c1 = 0.693121791f, c0 = 0.999999285f;
-  asm("{\n\t.reg .b64 x, n, f, p, k;\n\t.reg .b32 n0, n1;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 k, {%4, %4};\n\tadd.rn.f32x2 n, x, k;\n\t"
-      "mov.b64 k, {%5, %5};\n\tadd.rn.f32x2 f, n, k;\n\t"
-      "mov.b64 k, {%6, %6};\n\tfma.rn.f32x2 f, f, k, x;\n\t"
-      "mov.b64 p, {%7, %7};\n\t"
-      "mov.b64 k, {%8, %8};\n\tfma.rn.f32x2 p, p, f, k;\n\t"
-      "mov.b64 k, {%9, %9};\n\tfma.rn.f32x2 p, p, f, k;\n\t"
-      "mov.b64 k, {%10, %10};\n\tfma.rn.f32x2 p, p, f, k;\n\t"
-      "mov.b64 k, {%11, %11};\n\tfma.rn.f32x2 p, p, f, k;\n\t"
-      "mov.b64 {n0, n1}, n;\n\tshl.b32 n0, n0, 23;\n\tshl.b32 n1, n1, 23;\n\tmov.b64 n, {n0, n1};\n\t"
-      "mul.rn.f32x2 p, p, n;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(p0), "=f"(p1)
-      : "f"(x0), "f"(x1), "f"(kMagic), "f"(-kMagic), "f"(-1.f), "f"(c4), "f"(c3), "f"(c2), "f"(c1), "f"(c0));
 }
 
 // All lanes of the warp wait for `parity` on `bar`: lane 0 decides (bounded), then every lane
