@@ -120,8 +120,10 @@ def _ptr(t):
         return None
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(t, "ctypes"):
         return t.ctypes.data
     raise TypeError(type(t))
@@ -496,14 +498,20 @@ def _rope_cfg(cfg):
     return cfg if isinstance(cfg, zo_rope_cfg) else zo_rope_cfg.from_dict(cfg)
 
 
+_dtypes = {}
+
+
 def _dtype(t, dtype):
     """ZO_F32 / ZO_BF16 of a tensor, unless given."""
     if dtype is not None:
         return int(dtype)
-    import torch
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: ZO_F32, torch.bfloat16: ZO_BF16})
+    code = _dtypes.get(t.dtype)
+    if code is None:
         raise TypeError(f"{t.dtype}: float32 or bfloat16 expected")
-    return ZO_F32 if t.dtype == torch.float32 else ZO_BF16
+    return code
 
 
 def zo_rope_frequencies(cfg):

@@ -321,8 +321,10 @@ logprobs_kernel(const LogprobArgs a) {
   const RowView<T> row(static_cast<const T *>(a.logits) + r * a.ld, a.vocab);
   const int j_first = (int)((int64_t)row.vectors * part / a.splits);
   const int j_end = (int)((int64_t)row.vectors * (part + 1) / a.splits);
+  tc::pdl_launch_dependents();
   if (tid == 0) sh.n_hot = sh.n_cand = 0;
   if (a.splits > 1) tc::cluster_arrive();  // block 0 has to run before its memory is written
+  tc::pdl_wait();
   // the given token's logit, wanted at the end
   int32_t target = -1;
   float target_logit = 0.f;
@@ -543,21 +545,19 @@ logprobs_kernel(const LogprobArgs a) {
 
 template <typename T, int THREADS>
 cudaError_t launch_one(const LogprobArgs &a, int64_t rows, cudaStream_t st) {
-  if (a.splits == 1) {
-    constexpr int kRows = rows_of_block(THREADS);
-    logprobs_kernel<T, THREADS><<<(unsigned)((rows + kRows - 1) / kRows), dim3(THREADS, kRows), 0, st>>>(a);
-    return cudaGetLastError();
-  }
+  constexpr int kRows = rows_of_block(THREADS);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(rows * a.splits));
-  cfg.blockDim = dim3(THREADS);
+  cfg.gridDim = dim3((unsigned)(a.splits > 1 ? rows * a.splits : (rows + kRows - 1) / kRows));
+  cfg.blockDim = dim3(THREADS, kRows);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];  // may start before its predecessor's end (pdl_wait); clusters
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a);
 }
 

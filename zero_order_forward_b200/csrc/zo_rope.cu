@@ -6,24 +6,26 @@
 // the interleaved one (2 i with 2 i + 1).  The frequencies, scaled for long contexts or not, are
 // computed in fp64 on the host and travel as a kernel parameter.
 //
-// A block takes R rows.  Its threads first compute the rows' cosines and sines, once per (row,
-// pair) and not per head, into shared memory: position x (f_i / 2 pi) in fp64, the fraction of a
-// turn kept (exact enough at any int32 position: the product carries 53 bits, at most 31 of them
-// before the point), then sincospi in fp32.  Then every group of threads that covers one head
-// takes heads of the R rows in turn: 16 bytes of each half (half layout) or 16 bytes
-// (interleaved) per thread.
+// A group of threads covers one head, 16 bytes of each half (half layout) or 16 bytes (interleaved) a
+// thread, and takes kHeads heads of one row: their loads are under way before the thread computes
+// the cosines and sines of its own pairs, once for those heads: position x (f_i / 2 pi) in fp64, the
+// fraction of a turn kept (exact enough at any int32 position: the product carries 53 bits, at most
+// 31 of them before the point), then sincospi in fp32.  Computing them again for every kHeads heads
+// costs less than a block that computes them once, waits and shares them: 8192 rows of 24 heads of
+// 128 took 22.3 us that way.
 // Bound: HBM, two passes over the rotated heads.
 #include <cmath>
 #include <cstring>
 
 #include "zo_internal.cuh"
+#include "zo_tc.cuh"
 
 namespace zo {
 namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = ZO_ROPE_MAX_HEAD_DIM / 2;
-constexpr int kMaxRows = 16;  // rows of a block: kMaxRows x kMaxPairs float2 of shared memory
+constexpr int kHeads = 4;  // heads of a group of threads
 
 struct RopeArgs {
   const void *x;
@@ -31,10 +33,8 @@ struct RopeArgs {
   const int32_t *positions;
   int64_t rows, ldx, ldo;
   int heads, head_dim, pairs;
-  int units;       // threads that cover one head
-  int rot_units;   // of them, those that rotate (the others copy features behind rot_dim)
-  int rows_block;  // R
-  int heads_block; // heads of a block (blockIdx.y takes the next ones)
+  int units;      // threads that cover one head
+  int rot_units;  // of them, those that rotate (the others copy features behind rot_dim)
   float magnitude;
   double turns[kMaxPairs];  // f_i / (2 pi): turns per position
 };
@@ -86,62 +86,69 @@ template <typename T> struct Pack<T, 1> {
 template <typename T, bool IL, int VEC>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 cs[kMaxRows * kMaxPairs];
   using P = Pack<T, VEC>;
   using Raw = typename P::Raw;
-  const int64_t row0 = (int64_t)blockIdx.x * a.rows_block;
-  const int rows = (int)min((int64_t)a.rows_block, a.rows - row0);
-  for (int i = threadIdx.x; i < rows * a.pairs; i += kRopeThreads) {
-    const int r = i / a.pairs, f = i - r * a.pairs;
-    const int64_t row = row0 + r;
-    const double t = (a.positions ? (double)a.positions[row] : (double)row) * a.turns[f];
-    float s, c;
-    sincospif(2.f * (float)(t - rint(t)), &s, &c);
-    cs[i] = make_float2(c * a.magnitude, s * a.magnitude);
-  }
-  __syncthreads();
+  constexpr bool kOne = IL && VEC > 1;           // a pair's features lie in one access
+  constexpr int kPairs = kOne ? VEC / 2 : VEC;  // of a unit
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
   const int group = threadIdx.x / a.units, unit = threadIdx.x - group * a.units;
   const int groups = kRopeThreads / a.units;
-  if (group >= groups) return;
-  const int head0 = blockIdx.y * a.heads_block;
-  const int heads = min(a.heads_block, a.heads - head0);
-  const T *x = static_cast<const T *>(a.x);
-  T *out = static_cast<T *>(a.out);
-  const int half = a.pairs;  // distance of a pair's features in the half layout
-  for (int p = group; p < rows * heads; p += groups) {
-    const int r = p / heads, h = head0 + p - r * heads;
-    const T *xi = x + (row0 + r) * a.ldx + (int64_t)h * a.head_dim;
-    T *oi = out + (row0 + r) * a.ldo + (int64_t)h * a.head_dim;
-    const float2 *c = cs + r * a.pairs;
-    if (unit >= a.rot_units) {
-      const int f = 2 * a.pairs + (unit - a.rot_units) * VEC;
-      *reinterpret_cast<Raw *>(oi + f) = *reinterpret_cast<const Raw *>(xi + f);
-    } else if (IL && VEC > 1) {
-      const int f = unit * VEC;
-      float u[VEC];
-      P::open(*reinterpret_cast<const Raw *>(xi + f), u);
+  const int64_t row = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * groups + group;
+  if (group >= groups || row >= a.rows) return;
+  const int head0 = blockIdx.x * kHeads, heads = min(kHeads, a.heads - head0);
+  const bool turns = unit < a.rot_units;  // the other units copy features behind rot_dim
+  // the unit's first access, and its second in the rotating part
+  const int fa = !turns ? 2 * a.pairs + (unit - a.rot_units) * VEC : IL && VEC == 1 ? 2 * unit : unit * VEC;
+  const int fb = IL ? fa + 1 : fa + a.pairs;
+  const T *xi = static_cast<const T *>(a.x) + row * a.ldx + (int64_t)head0 * a.head_dim;
+  T *oi = static_cast<T *>(a.out) + row * a.ldo + (int64_t)head0 * a.head_dim;
+  const double pos = a.positions ? (double)a.positions[row] : (double)row;
+  Raw first[kHeads], second[kHeads];
 #pragma unroll
-      for (int i = 0; i < VEC; i += 2) {
-        const float2 w = c[(f + i) / 2];
-        const float va = u[i], vb = u[i + 1];
-        u[i] = va * w.x - vb * w.y;
-        u[i + 1] = vb * w.x + va * w.y;
-      }
-      *reinterpret_cast<Raw *>(oi + f) = P::close(u);
-    } else {
-      const int fa = IL ? 2 * unit : unit * VEC, fb = IL ? fa + 1 : fa + half;
+  for (int h = 0; h < kHeads; ++h) {
+    if (h < heads) {
+      first[h] = *reinterpret_cast<const Raw *>(xi + h * a.head_dim + fa);
+      if (!kOne && turns) second[h] = *reinterpret_cast<const Raw *>(xi + h * a.head_dim + fb);
+    }
+  }
+  if (!turns) {
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+      if (h < heads) *reinterpret_cast<Raw *>(oi + h * a.head_dim + fa) = first[h];
+    return;
+  }
+  float c[kPairs], s[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const double t = pos * a.turns[unit * kPairs + i];
+    sincospif(2.f * (float)(t - rint(t)), &s[i], &c[i]);
+    c[i] *= a.magnitude;
+    s[i] *= a.magnitude;
+  }
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    if (h < heads) {
       float u[VEC], v[VEC];
-      P::open(*reinterpret_cast<const Raw *>(xi + fa), u);
-      P::open(*reinterpret_cast<const Raw *>(xi + fb), v);
+      P::open(first[h], u);
+      if (kOne) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float2 w = c[unit * VEC + i];
-        const float va = u[i], vb = v[i];
-        u[i] = va * w.x - vb * w.y;
-        v[i] = vb * w.x + va * w.y;
+        for (int i = 0; i < kPairs; ++i) {
+          const float va = u[2 * i], vb = u[2 * i + 1 < VEC ? 2 * i + 1 : 0];
+          u[2 * i] = va * c[i] - vb * s[i];
+          u[2 * i + 1 < VEC ? 2 * i + 1 : 0] = vb * c[i] + va * s[i];
+        }
+      } else {
+        P::open(second[h], v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float va = u[i], vb = v[i];
+          u[i] = va * c[i] - vb * s[i];
+          v[i] = vb * c[i] + va * s[i];
+        }
+        *reinterpret_cast<Raw *>(oi + h * a.head_dim + fb) = P::close(v);
       }
-      *reinterpret_cast<Raw *>(oi + fa) = P::close(u);
-      *reinterpret_cast<Raw *>(oi + fb) = P::close(v);
+      *reinterpret_cast<Raw *>(oi + h * a.head_dim + fa) = P::close(u);
     }
   }
 }
@@ -158,26 +165,15 @@ cudaError_t launch(RopeArgs &a, bool interleaved, bool in_place, cudaStream_t st
   const int vec = wide ? kVec : 1;
   a.rot_units = interleaved && wide ? 2 * a.pairs / vec : a.pairs / vec;
   a.units = a.rot_units + (in_place ? 0 : rest / vec);
-  const int groups = kRopeThreads / a.units;
-  // A block's threads take about four heads each; its rows share the grid's other dimension when
-  // one row has more than that.
-  int64_t r = 4 * (int64_t)groups / a.heads;
-  r = r < 1 ? 1 : r > kMaxRows ? kMaxRows : r;
-  const int64_t spread = (a.rows + 2 * kSmCount - 1) / (2 * kSmCount);  // fill the SMs first
-  if (r > spread) r = spread;
-  a.rows_block = (int)r;
-  a.heads_block = a.heads;
-  if (r == 1 && a.heads > 4 * groups) a.heads_block = 4 * groups;
-  const unsigned gy = (unsigned)((a.heads + a.heads_block - 1) / a.heads_block);
-  const dim3 grid((unsigned)((a.rows + r - 1) / r), gy);
-  if (interleaved) {
-    if (wide) rope_kernel<T, true, kVec><<<grid, kRopeThreads, 0, st>>>(a);
-    else rope_kernel<T, true, 1><<<grid, kRopeThreads, 0, st>>>(a);
-  } else {
-    if (wide) rope_kernel<T, false, kVec><<<grid, kRopeThreads, 0, st>>>(a);
-    else rope_kernel<T, false, 1><<<grid, kRopeThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  const int64_t groups = kRopeThreads / a.units, blocks = (a.rows + groups - 1) / groups;
+  // row blocks over y and z
+  const int64_t y = blocks < 65535 ? blocks : 65535;
+  const dim3 grid((unsigned)((a.heads + kHeads - 1) / kHeads), (unsigned)y, (unsigned)((blocks + y - 1) / y));
+  if (interleaved)
+    return wide ? launch_early(rope_kernel<T, true, kVec>, grid, kRopeThreads, 0, st, a)
+                : launch_early(rope_kernel<T, true, 1>, grid, kRopeThreads, 0, st, a);
+  return wide ? launch_early(rope_kernel<T, false, kVec>, grid, kRopeThreads, 0, st, a)
+              : launch_early(rope_kernel<T, false, 1>, grid, kRopeThreads, 0, st, a);
 }
 
 // Why `c` is not a rotary configuration, or null.
@@ -199,17 +195,24 @@ const char *rope_cfg_error(const zo_rope_cfg &c) {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
-// Frequency i of a valid configuration, radians per position.
-double rope_frequency(const zo_rope_cfg &c, int i) {
-  const double f = std::pow((double)c.theta, -2.0 * i / c.rot_dim);
-  if (c.scaling == ZO_ROPE_LINEAR) return f / (double)c.factor;
-  if (c.scaling == ZO_ROPE_BANDS) {
-    const double turns = (double)c.orig_len * f / kTwoPi;
-    double g = (turns - (double)c.band_low) / ((double)c.band_high - (double)c.band_low);
-    g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
-    return g * f + (1.0 - g) * f / (double)c.factor;
+// The rot_dim / 2 frequencies of a valid configuration, radians per position: theta^(-2 i / rot_dim) as
+// the product of one of 16 steps of eight i and one of eight steps of one (three roundings of
+// 2^-53; the powers are most of what this call costs).
+void rope_frequencies(const zo_rope_cfg &c, double *f) {
+  double step[8];
+  for (int i = 0; i < 8; ++i) step[i] = std::pow((double)c.theta, -2.0 * i / c.rot_dim);
+  double block = 1.0;
+  for (int i = 0; i < c.rot_dim / 2; ++i) {
+    if (i % 8 == 0) block = std::pow((double)c.theta, -2.0 * i / c.rot_dim);
+    f[i] = block * step[i % 8];
+    if (c.scaling == ZO_ROPE_LINEAR) f[i] /= (double)c.factor;
+    if (c.scaling == ZO_ROPE_BANDS) {
+      const double turns = (double)c.orig_len * f[i] / kTwoPi;
+      double g = (turns - (double)c.band_low) / ((double)c.band_high - (double)c.band_low);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f[i] = g * f[i] + (1.0 - g) * f[i] / (double)c.factor;
+    }
   }
-  return f;
 }
 
 }  // namespace
@@ -221,7 +224,7 @@ extern "C" {
 
 zo_status zo_rope_frequencies(const zo_rope_cfg *cfg, double *radians) {
   if (!cfg || !radians || rope_cfg_error(*cfg)) return ZO_ERR_INVALID;
-  for (int i = 0; i < cfg->rot_dim / 2; ++i) radians[i] = rope_frequency(*cfg, i);
+  rope_frequencies(*cfg, radians);
   return ZO_OK;
 }
 
@@ -257,7 +260,8 @@ zo_status zo_rope(zo_ctx *ctx, const void *x, void *out, int dtype, const int32_
   a.head_dim = head_dim;
   a.pairs = cfg->rot_dim / 2;
   a.magnitude = cfg->magnitude;
-  for (int i = 0; i < kMaxPairs; ++i) a.turns[i] = i < a.pairs ? rope_frequency(*cfg, i) / kTwoPi : 0.0;
+  rope_frequencies(*cfg, a.turns);
+  for (int i = 0; i < a.pairs; ++i) a.turns[i] *= 1.0 / kTwoPi;
   const cudaError_t e = dtype == ZO_F32 ? launch<float>(a, cfg->interleaved != 0, x == out, ctx->stream)
                                         : launch<uint16_t>(a, cfg->interleaved != 0, x == out, ctx->stream);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "rope_kernel: %s", cudaGetErrorString(e));
