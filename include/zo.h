@@ -676,7 +676,7 @@ zo_status zo_rope(zo_ctx *ctx, const void *x, void *out, int dtype, const int32_
  * rows hold (infinities and NaN too).  The offsets are read on the device: a decreasing or
  * out-of-range pair raises ZO_FLAG_OFFSETS (seen by zo_sync) and its sequence is skipped.
  * n_heads % n_kv_heads == 0, head_dim 64 or 128, pointers 16-byte aligned, row strides multiples
- * of 8 elements, 1 <= total_tokens < 2^31, 1 <= n_seqs.  Bounded waits as zo_gemm_bf16.
+ * of 8 elements, 1 <= total_tokens < 2^31 - 256, 1 <= n_seqs <= 2^24.  Bounded waits as zo_gemm_bf16.
  * Errors: ZO_ERR_INVALID, ZO_ERR_UNSUPPORTED (head_dim), ZO_ERR_CUDA. */
 zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void *k, const void *v, void *out,
                               const int32_t *cu_seqlens, int32_t n_seqs, int64_t total_tokens,
@@ -718,9 +718,8 @@ zo_status zo_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t *bytes
  *   targets, logprob, entropy  as zo_logprobs (at least one output).
  *   workspace  device, 16-byte aligned, zo_head_logprobs_workspace bytes; holds nothing between
  *              calls.  Calls that may run at the same time need one each.
- * Logits within +-1e8; a row with a NaN or +inf among its logits has NaN outputs, one with a -inf
- * a NaN entropy.  width, ldh and ldw multiples of 8, hidden and W 16-byte aligned, rows, vocab,
- * width, ldh, ldw >= 1 and < 2^31.  Bounded waits as zo_gemm_bf16.  Errors: ZO_ERR_INVALID (also a
+ * Finite logits within +-1e8; -inf, NaN and +inf as in zo_logprobs.  width, ldh and ldw multiples
+ * of 8, hidden and W 16-byte aligned, rows, vocab, width, ldh, ldw >= 1 and < 2^31.  Bounded waits as zo_gemm_bf16.  Errors: ZO_ERR_INVALID (also a
  * workspace that is too small), ZO_ERR_CUDA. */
 zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64_t rows, int64_t vocab,
                            int64_t width, int64_t ldh, int64_t ldw, const int32_t *targets,

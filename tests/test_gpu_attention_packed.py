@@ -84,7 +84,8 @@ LENS = [[1], [2], [17], [64], [65], [127], [128], [129], [191, 1, 0, 193], [256,
 
 
 @pytest.mark.parametrize("lens", LENS, ids=lambda v: "-".join(map(str, v[:6])))
-@pytest.mark.parametrize("H,Hk,hd", [(4, 2, 128), (3, 3, 64), (8, 1, 64), (1, 1, 128)])
+@pytest.mark.parametrize("H,Hk,hd", [(4, 2, 128), (3, 3, 64), (8, 1, 64), (1, 1, 128), (4, 4, 64), (6, 2, 64),
+                                     (2, 2, 128), (6, 2, 128)])
 def test_packed_attention_matches(zo, ctx, lens, H, Hk, hd):
     qkv = make(lens, H, Hk, hd)
     out = torch.zeros(max(1, sum(lens)), H * hd, dtype=torch.bfloat16, device="cuda")
@@ -265,6 +266,44 @@ def test_bad_offsets_raise_the_flag_and_are_skipped(zo, ctx, cu, kept):
         assert torch.all((out[a:b].double() - ref).abs() <= tol)
 
 
+@pytest.mark.parametrize("H,Hk,hd", [(2, 2, 64), (2, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_bad_rows_stay_out_however_heads_are_paired(zo, ctx, H, Hk, hd, what):
+    """Neighbour sequences, padding and a later token full of NaN or infinities, with pairs of heads
+    that share no key/value head and with two tiles of one head."""
+    lens, late = [100, 30, 300, 64, 3, 390], 250
+    qkv = make(lens, H, Hk, hd, extra=150)
+    clean = qkv.clone()
+    at = np.cumsum([0] + lens)
+    qkv[at[1]: at[2]] = what
+    qkv[at[3]: at[4]] = what
+    qkv[at[2] + late, H * hd:] = what          # a key and value row of the third sequence
+    qkv[at[-1]:] = what
+    out = torch.full((len(qkv), H * hd), 3.0, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets(lens), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    q, k, v = split(clean, H, Hk, hd)
+    ref, tol = reference(q, k, v, lens, H, Hk, hd, 1 / math.sqrt(hd))
+    err = (out[: at[-1]].double() - ref).abs()
+    for i in (0, 4, 5):
+        assert torch.all(err[at[i]: at[i + 1]] <= tol[at[i]: at[i + 1]])
+    assert torch.all(err[at[2]: at[2] + late] <= tol[at[2]: at[2] + late])
+    assert torch.all(out[at[-1]:] == 3.0)
+
+
+@pytest.mark.parametrize("H,Hk,hd", [(4, 2, 128), (4, 4, 64), (3, 3, 64)])
+def test_many_sequences_of_several_tiles(zo, ctx, H, Hk, hd):
+    """More than 32 sequences with up to four tiles: several rounds of items on every CTA."""
+    r = np.random.default_rng(1)
+    lens = r.integers(0, 450, 110).tolist()
+    qkv = make(lens, H, Hk, hd, extra=9)
+    out = torch.full((len(qkv), H * hd), 3.0, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets(lens), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    check(zo, ctx, qkv, out, lens, H, Hk, hd)
+    assert torch.all(out[sum(lens):] == 3.0)
+
+
 def test_two_graphs_of_one_context_and_changed_lengths(zo):
     """Captured once, replayed with other offsets in the same buffers; two graphs in turn."""
     s = torch.cuda.Stream()
@@ -316,6 +355,7 @@ def test_packed_attention_refusals(zo, ctx):
         refused(**{name: 120})
         refused(**{name: 388})
     refused(n=0)
+    refused(n=(1 << 24) + 1)
     refused(total=0)
     refused(total=1 << 31)
     refused(H=0)

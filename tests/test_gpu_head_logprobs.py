@@ -68,7 +68,8 @@ def check(h, w, t, got):
 
 SIZES = [(1, 1, 8), (1, 2, 8), (3, 31, 16), (5, 32, 64), (1, 33, 72), (7, 257, 128), (127, 1000, 64), (128, 4736, 64),
          (129, 5000, 136), (16, 50272, 768), (1, 30001, 1024), (200, 9999, 512), (300, 500, 264), (1000, 3001, 64),
-         (2049, 1200, 128), (513, 40000, 192), (4096, 20011, 64)]
+         (2049, 1200, 128), (513, 40000, 192), (4096, 20011, 64), (5, 1000, 1032), (200, 3000, 2056), (130, 1000, 4096),
+         (257, 64, 8), (129, 63, 1024)]
 
 
 @pytest.mark.parametrize("rows,vocab,width", SIZES)
@@ -124,6 +125,40 @@ def test_bad_rows_stay_their_own(zo, ctx, rows):
     assert torch.isnan(lp[[2, 4]]).all() and torch.isnan(ent[[2, 4]]).all()
     keep = [i for i in range(rows) if i not in (2, 4)]
     assert torch.equal(lp[keep], want[0][keep]) and torch.equal(ent[keep], want[1][keep])
+
+
+@pytest.mark.parametrize("rows", [9, 500])
+@pytest.mark.parametrize("where", [0, 31, 1000, 1984, 1999])
+@pytest.mark.parametrize("count", [1, 40, 600])
+def test_a_bad_row_of_the_head_is_seen_by_every_row(zo, ctx, rows, where, count):
+    """NaN in one or many rows of W, whole ranges of a CTA among them."""
+    h, w, t = make(rows, 2000, 128)
+    w[where: where + count] = math.nan
+    lp, ent = call(zo, ctx, h, w, t)
+    assert torch.isnan(lp).all() and torch.isnan(ent).all()
+
+
+@pytest.mark.parametrize("rows", [9, 500])
+@pytest.mark.parametrize("where,count", [(0, 1), (100, 40), (1300, 700)])
+def test_ruled_out_tokens_leave_the_others_scores(zo, ctx, rows, where, count):
+    """W rows that give a logit of -inf: probability 0, as if they were not there; a row without any
+    other has no distribution."""
+    h, w, t = make(rows, 2000, 128)
+    h[:, 0] = 1.0
+    w[where: where + count] = 0.0
+    w[where: where + count, 0] = -math.inf
+    t[:] = torch.arange(rows, device="cuda") % 50 + 50
+    got = call(zo, ctx, h, w, t)
+    keep = torch.ones(2000, dtype=torch.bool, device="cuda")
+    keep[where: where + count] = False
+    tk = (torch.cumsum(keep.int(), 0) - 1)[t.long()].to(torch.int32)
+    check(h, w[keep], tk, got)
+    t[:] = where
+    lp, _ = call(zo, ctx, h, w, t)
+    assert torch.all(lp == -math.inf)
+    w[:] = w[where]
+    lp, ent = call(zo, ctx, h, w, t)
+    assert torch.isnan(lp).all() and torch.isnan(ent).all()
 
 
 @pytest.mark.parametrize("rows", [4, 900])

@@ -138,6 +138,48 @@ def test_largest_logits_crowded_into_few_places(zo, ctx, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,rows", [(20000, 200), (3000, 160), (700, 30)])
+def test_ties_masks_and_bad_rows_where_a_block_has_a_row_of_its_own(zo, ctx, dtype, n, rows):
+    """The same kinds of rows with enough of them that none is split, and with rows of one warp."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    at = torch.arange(n, device="cuda")
+    low = torch.finfo(TYPES[dtype]).min
+    kinds = [torch.zeros(n, device="cuda"), torch.randint(0, 3, (n,), generator=g, device="cuda").float(),
+             at.float().div(100).floor(), -at.float().div(n // 5).floor(), torch.where(at == n - 1, 0.0, -math.inf),
+             torch.where(at % 97 == 5, at.float() / n, torch.full((n,), -math.inf, device="cuda")),
+             torch.full((n,), low, device="cuda"), torch.where((at // 8) % 128 < 9, 10.0 + (at % 7).float(), 0.0)]
+    x = torch.stack([kinds[i % len(kinds)] for i in range(rows)]).to(TYPES[dtype])
+    t = torch.full((rows,), n - 1, dtype=torch.int32, device="cuda")
+    for top in (5, 32):
+        check(x, t, call(zo, ctx, x, t, top), top)
+    x[3, n // 2] = math.nan
+    x[11, 0] = math.inf
+    x[rows - 1] = -math.inf
+    lp, ent, ids, tlp = call(zo, ctx, x, t, 2)
+    bad = [3, 11, rows - 1]
+    assert torch.isnan(lp[bad]).all() and torch.isnan(ent[bad]).all() and torch.isnan(tlp[bad]).all()
+    assert ids[3, 0] == n // 2 and ids[11, 0] == 0 and ids[rows - 1].tolist() == [0, 1]
+    keep = [i for i in range(rows) if i not in bad]
+    check(x[keep], t[keep], (lp[keep], ent[keep], ids[keep], tlp[keep]), 2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(1, 4099), (3, 9000), (40, 8300), (148, 5000), (149, 5000)])
+@pytest.mark.parametrize("shift", [0, 3])
+def test_rows_split_over_blocks(zo, ctx, dtype, rows, vocab, shift):
+    """A row's largest logits, masks and target in each of its parts."""
+    x, t = logits(rows, vocab + 16, dtype, seed=shift)
+    x = x[:, shift: shift + vocab]
+    at = torch.linspace(0, vocab - 1, 9, device="cuda").long()
+    x[:, at[:-1]] += torch.randperm(8, device="cuda").to(x.dtype) + 9
+    x[0, vocab // 3: vocab // 2] = -math.inf
+    t = at[torch.arange(rows, device="cuda") % 9].to(torch.int32)
+    lp, ent, ids, tlp = buffers(rows, 7)
+    zo.zo_logprobs(ctx, x, rows, vocab, x.stride(0), t, lp, ent, 7, ids, tlp)
+    check(x, t, (lp, ent, ids, tlp), 7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_masked_rows(zo, ctx, dtype):
     """-inf and the type's lowest value as masks; one token left; rows that only masks fill."""
     n, low = 9000, torch.finfo(TYPES[dtype]).min

@@ -130,6 +130,21 @@ def test_rope_query_and_key_heads_of_a_fused_projection_as_the_model_rotates(zo,
     assert torch.equal(bad, expect)
 
 
+def test_rope_more_rows_than_a_grid_dimension(zo, ctx):
+    """One row to a block and more of them than 65535 (heads of 256 that are not 16-byte aligned)."""
+    rows, hd = 65535 + 700, 256
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(rows, hd + 1, generator=g, device="cuda")
+    out = torch.zeros(rows, hd, device="cuda")
+    cfg = dict(theta=1.0e4, rot_dim=hd)
+    zo.zo_rope(ctx, x, out, None, cfg, rows, hd + 1, hd, 1, hd)
+    part = list(range(40)) + list(range(65500, 65600)) + list(range(rows - 40, rows))
+    want = torch.zeros(len(part), hd, device="cuda")
+    zo.zo_rope(ctx, x[part].contiguous(), want, torch.tensor(part, dtype=torch.int32, device="cuda"), cfg, len(part),
+               hd + 1, hd, 1, hd)
+    assert torch.equal(out[part], want) and torch.all(out.abs().sum(1) > 0)
+
+
 def test_rope_on_another_stream_and_replayed(zo):
     """A context on its own stream, its call captured once and replayed on changed inputs."""
     s = torch.cuda.Stream()

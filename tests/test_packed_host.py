@@ -96,36 +96,54 @@ def test_head_workspace_is_far_below_the_logits(zo, vocab):
     assert last == n
 
 
-def _find_tile(cu, total, slot):
-    """find_tile of the packed attention: (first row, length, query tile) or length 0."""
-    base = 0
+def _items(cu, total, rows, group, grid):
+    """The items that each CTA of the packed attention takes, in its order: (sequence, tile, head group)
+    by falling tile number, heads fastest, to and fro over the CTAs, a last partial round from the back."""
+    tiles = []
     for s, e in zip(cu[:-1], cu[1:]):
-        if s < 0 or e < s or e > total:
-            s = e = 0
-        n = (e - s + 127) // 128
-        if base + n > slot:
-            return s, e - s, slot - base
-        base += n
-    return 0, 0, 0
+        bad = s < 0 or e < s or e > total
+        tiles.append(0 if bad else (e - s + rows - 1) // rows)
+    count = sum(tiles) * group
+    for cta in range(grid):
+        level = max(tiles) - 1
+        base = n = 0
+        while True:
+            back = n % 2 == 1 or (n > 0 and (n + 1) * grid >= count)
+            slot = n * grid + (grid - 1 - cta if back else cta)
+            n += 1
+            while level >= 0 and slot >= base + sum(t > level for t in tiles) * group:
+                base += sum(t > level for t in tiles) * group
+                level -= 1
+            if level < 0:
+                break
+            index = slot - base
+            yield cta, [i for i, t in enumerate(tiles) if t > level][index // group], level, index % group
 
 
-@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 5], [128, 129, 127], [1] * 300, [0, 1000, 0, 1, 2]])
-@pytest.mark.parametrize("extra", [0, 5])
-def test_every_query_row_is_in_exactly_one_block(lens, extra):
-    """ceil(total / 128) + n_seqs blocks cover every tile of every sequence once."""
+@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 5], [128, 129, 127], [1] * 300, [0, 1000, 0, 1, 2],
+                                  [2000, 3, 700, 700, 128, 256, 257]])
+@pytest.mark.parametrize("rows,group", [(128, 3), (256, 2)])
+def test_every_tile_of_every_sequence_is_one_item(lens, rows, group):
     cu = [0] + np.cumsum(lens).tolist()
-    total = max(1, cu[-1] + extra)
-    seen = np.zeros(total, int)
-    for slot in range((total + 127) // 128 + len(lens)):
-        row0, n, qt = _find_tile(cu, total, slot)
-        if n:
-            seen[row0 + 128 * qt: row0 + min(n, 128 * qt + 128)] += 1
-    assert np.all(seen[: cu[-1]] == 1) and np.all(seen[cu[-1]:] == 0)
+    total = max(1, cu[-1])
+    most = ((total + rows - 1) // rows + len(lens)) * group
+    for grid in (min(148, most), min(7, most)):
+        seen = [(s, t, g) for _, s, t, g in _items(cu, total, rows, group, grid)]
+        want = [(s, t, g) for s, n in enumerate(lens) for t in range((n + rows - 1) // rows) for g in range(group)]
+        assert sorted(seen) == want
+
+
+def test_long_items_are_spread():
+    """The work (key tiles) of the busiest CTA stays near the mean."""
+    lens = [2048, 129, 1777, 64, 1023, 2000, 300, 5]
+    cu = [0] + np.cumsum(lens).tolist()
+    load = np.zeros(148)
+    for cta, _, tile, _ in _items(cu, cu[-1], 128, 6, 148):
+        load[cta] += tile + 1
+    assert load.max() <= 1.2 * load.mean()
 
 
 @pytest.mark.parametrize("cu", [[0, 10, 5, 20], [-3, 10, 20], [0, 10, 40], [2 ** 31 - 1, -2 ** 31, 4]])
-def test_bad_offsets_never_leave_the_buffer(cu):
-    total = 32
-    for slot in range(1 + len(cu)):
-        row0, n, qt = _find_tile(cu, total, slot)
-        assert 0 <= row0 and row0 + n <= total
+def test_bad_offsets_have_no_items(cu):
+    good = {i for i, (s, e) in enumerate(zip(cu[:-1], cu[1:])) if 0 <= s <= e <= 32}
+    assert {s for _, s, _, _ in _items(cu, 32, 128, 1, 4)} == {i for i in good if cu[i + 1] > cu[i]}

@@ -121,6 +121,7 @@ struct Schedule {
   int first_row, first_len;
   int level, count;        // sequences with more than `level` tiles: `count`
   int64_t base, total;     // items of the longer levels; of all
+  int longest;             // tiles of the longest sequence
   int from, before;        // sequences [0, from) have `before` of the level's
   __device__ __forceinline__ Schedule(const PackedArgs &args) : a(args) {
     lane = threadIdx.x & 31;
@@ -143,7 +144,8 @@ struct Schedule {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, o);
     total = tiles * group;
-    level = __reduce_max_sync(0xFFFFFFFFu, most) - 1;
+    longest = __reduce_max_sync(0xFFFFFFFFu, most);
+    level = longest - 1;
     base = 0;
     count = level >= 0 ? sequences() : 0;
   }
@@ -545,7 +547,12 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         const bool back = (n & 1) || (n > 0 && (int64_t)(n + 1) * gridDim.x >= sched.total);
         const int64_t c = back ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
         const Item it = sched.at((int64_t)n * gridDim.x + c);
-        if (!tc::warp_wait_fast(&item_empty[n % kItems], ring_parity(n, kItems) ^ 1u, abort_flag)) {
+        // an item takes its tiles' time: one wait for every 2^18 of them (about 0.4 s)
+        int waits = 1 + (sched.longest >> 18);
+        bool ok = false;
+        while (!ok && waits-- > 0 && !*abort_flag)
+          ok = tc::warp_wait_fast(&item_empty[n % kItems], ring_parity(n, kItems) ^ 1u, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
           if (lane == 0) give_up();
           break;
         }
@@ -696,8 +703,8 @@ extern "C" zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void 
     return fail(ctx, ZO_ERR_UNSUPPORTED, "attention_packed: head_dim must be 64 or 128");
   if (n_heads < 1 || n_heads > 65535 || n_kv_heads < 1 || n_heads % n_kv_heads)
     return fail(ctx, ZO_ERR_INVALID, "attention_packed: n_kv_heads must divide n_heads (1 .. 65535)");
-  if (n_seqs < 1 || total_tokens < 1 || total_tokens > INT32_MAX - 256 || n_seqs > INT32_MAX / 2)
-    return fail(ctx, ZO_ERR_INVALID, "attention_packed: need n_seqs >= 1 and total_tokens in [1, 2^31 - 257]");
+  if (n_seqs < 1 || n_seqs > 1 << 24 || total_tokens < 1 || total_tokens > INT32_MAX - 256)
+    return fail(ctx, ZO_ERR_INVALID, "attention_packed: need n_seqs in [1, 2^24] and total_tokens in [1, 2^31 - 257]");
   const int64_t wq = (int64_t)n_heads * head_dim, wk = (int64_t)n_kv_heads * head_dim;
   if (ldq < wq || ldo < wq || ldk < wk || ldv < wk || (ldq | ldk | ldv | ldo) % 8 || (ldq | ldk | ldv) >= ((int64_t)1 << 38))
     return fail(ctx, ZO_ERR_INVALID, "attention_packed: row strides must cover the heads and be multiples of 8");

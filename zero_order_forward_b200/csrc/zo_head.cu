@@ -25,10 +25,20 @@ namespace {
 
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
+// 2^t for t below -kLowest (that of a ruled out token's -inf, or of no column) is 0, and so is 2^t t.
+constexpr float kLowest = 1e30f;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kBox = 32;  // rows of W in one TMA box
 constexpr int kEpiWarps = 16;  // 4 for each quarter of a tile's columns: the exponentials need warps to wait for
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (4 + kEpiWarps);  // loads, MMAs, two idle ones; epilogue
+// Registers of a thread: 4 warps x kFew + 16 x kMany = 20 x 96 of the launch.
+constexpr int kFew = 32, kMany = 112;
+// The tensor cores truncate each addition to an fp32 accumulator: over a width of 2048 the entropy
+// came out off by 1.1e-6 and over 4096 by 2.1e-6, where rounded sums give 1e-7 to 9e-7.  So an
+// accumulator takes this many 64-wide steps, and the epilogue adds accumulators up, rounded: 16
+// steps leave 6e-7 and 1.3e-6 and cost 1% of the time at a width of 2048, 8 would leave 3e-7 and 6e-7
+// and cost 3.5%.
+constexpr int kChunk = 16;
 
 template <bool PAIR>
 struct HeadCfg {
@@ -73,13 +83,13 @@ struct RowStats {
   // These sums relative to `top` (a whole number, m at least), added to (s, u) there.
   __device__ __forceinline__ void add_to(float top, double &ts, double &tu) const {
     if (empty()) return;
-    const float d = m - top;
+    const float d = m == top ? 0.f : m - top;  // (both may be -inf)
     const double e = (double)tc::ex2(d);
     ts += e * s;
     tu += e * (u + (double)d * s);
   }
 
-  __device__ __forceinline__ void take(const float (&v)[32]) {
+  __device__ __forceinline__ void take(const float *v) {  // 32 columns
     float x4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
     for (int i = 4; i < 32; i += 8) {
@@ -103,6 +113,8 @@ struct RowStats {
     for (int i = 0; i < 32; i += 2) {
       float t0, t1;
       tc::fma2_bc(v[i], v[i + 1], kLog2E, -ref, t0, t1);
+      t0 = tc::max_nan(t0, -kLowest);
+      t1 = tc::max_nan(t1, -kLowest);
       const float p0 = tc::ex2(t0), p1 = tc::ex2(t1);
       const int h = i & 2;
       tc::add2(s4[h], s4[h + 1], p0, p1);
@@ -125,23 +137,37 @@ __device__ __forceinline__ void write_part(const HeadArgs &a, const RowStats *qu
   a.part[(int64_t)row * a.splits + split] = make_float4(r.m, (float)r.s, (float)r.u, 0.f);
 }
 
-// The columns [c0, c0 + 32) of the tile at W's row n0 (`cols` of them exist) of one row.
-__device__ __forceinline__ void take_chunk(RowStats &st, uint32_t taddr, int n0, int c0, int cols, int target,
-                                           float *target_logit) {
-  float v[32];
-  tc::tmem_ld32(taddr + (uint32_t)c0, v);
-  const int hit = target - (n0 + c0);
-  if (__any_sync(0xFFFFFFFFu, hit >= 0 && hit < 32)) {
-    float x = 0.f;
+// What an epilogue thread does with one accumulator: its row's 64 columns from taddr on, added to x.
+__device__ __forceinline__ void add_columns(float (&x)[64], uint32_t taddr, bool first) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x = i == hit ? v[i] : x;
-    if (hit >= 0 && hit < min(32, cols - c0)) *target_logit = x;
-  }
-  if (c0 + 32 > cols) {
+  for (int c = 0; c < 64; c += 16) {
+    float v[16];
+    tc::tmem_ld16(taddr + (uint32_t)c, v);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = c0 + i < cols ? v[i] : -1e30f;
+    for (int i = 0; i < 16; ++i) x[c + i] = first ? v[i] : x[c + i] + v[i];
   }
-  st.take(v);
+}
+
+// One row's logits of W's rows n0 .. n0 + 63, of which `cols` exist, into its statistics.
+__device__ __forceinline__ void take_columns(RowStats &st, float (&x)[64], int n0, int cols, int target,
+                                             float *target_logit) {
+#pragma unroll
+  for (int c = 0; c < 64; c += 32) {
+    if (c < cols) {
+      const int hit = target - (n0 + c);
+      if (__any_sync(0xFFFFFFFFu, hit >= 0 && hit < 32)) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v = i == hit ? x[c + i] : v;
+        if (hit >= 0 && hit < min(32, cols - c)) *target_logit = v;
+      }
+      if (c + 32 > cols) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[c + i] = c + i < cols ? x[c + i] : -INFINITY;
+      }
+      st.take(x + c);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -161,7 +187,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
   RowStats *stats = reinterpret_cast<RowStats *>(smem + S::kStatsOffset);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int m0 = blockIdx.x * kBM, split = blockIdx.y;
   const int n_first = range_first(split, a.units, a.splits, kUnit);
   const int n_last = min(range_first(split + 1, a.units, a.splits, kUnit), a.vocab);
@@ -191,84 +217,95 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   tc::pdl_wait();
 
   uint32_t issued = 0;
-  if (warp == 0 && lane == 0) {
-    tc::tma_prefetch_desc(&tmA);
-    tc::tma_prefetch_desc(&tmB);
-    for (int t = 0; t < tiles && !*abort_flag; ++t) {
-      const int boxes = tile_units(t);
-      for (int kb = 0; kb < nk; ++kb) {
-        const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
-        if (*abort_flag || !tc::mbar_wait(&empty[s], ph ^ 1u)) {
-          atomicOr(a.err, ZO_FLAG_TIMEOUT);
-          *abort_flag = 1;
-          break;
+  if (warp < 4) {
+    tc::regs_dec<kFew>();
+    if (warp == 0 && lane == 0) {
+      tc::tma_prefetch_desc(&tmA);
+      tc::tma_prefetch_desc(&tmB);
+      for (int t = 0; t < tiles && !*abort_flag; ++t) {
+        const int boxes = tile_units(t);
+        for (int kb = 0; kb < nk; ++kb) {
+          const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
+          if (*abort_flag || !tc::mbar_wait(&empty[s], ph ^ 1u)) {
+            atomicOr(a.err, ZO_FLAG_TIMEOUT);
+            *abort_flag = 1;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&full[s], (uint32_t)a.a_rows * kBK * 2 + (uint32_t)boxes * S::kBoxBytes);
+          tc::tma_load_2d(sA + s * S::kABytes, &tmA, &full[s], kb * kBK, m0);
+          for (int b = 0; b < boxes; ++b)
+            tc::tma_load_2d(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, &full[s], kb * kBK,
+                            n_first + t * kBN + b * kUnit);
+          ++issued;
         }
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)a.a_rows * kBK * 2 + (uint32_t)boxes * S::kBoxBytes);
-        tc::tma_load_2d(sA + s * S::kABytes, &tmA, &full[s], kb * kBK, m0);
-        for (int b = 0; b < boxes; ++b)
-          tc::tma_load_2d(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, &full[s], kb * kBK,
-                          n_first + t * kBN + b * kUnit);
-        ++issued;
       }
-    }
-    tc::pdl_launch_dependents();
-  } else if (warp == 1 && lane == 0) {
-    uint32_t consumed = 0;
-    for (int t = 0; t < tiles && !*abort_flag; ++t) {
-      const int b = t & 1;
-      if (!tc::mbar_wait(&acc_empty[b], ((uint32_t)(t >> 1) & 1u) ^ 1u)) {
+      tc::pdl_launch_dependents();
+    } else if (warp == 1) {  // MMAs: the warp in step, one lane issues
+      const uint32_t a0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sA), 0));
+      const uint32_t b0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sB), 0));
+      const uint32_t tm0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      tc::RingPos<kStages> pos;
+      uint32_t accs = 0;
+      bool ok = true;
+      for (int t = 0; ok && t < tiles; ++t) {
+        const uint32_t idesc = tc::idesc_bf16_f32(kBM, tile_units(t) * kUnit);
+        for (int k0 = 0; ok && k0 < nk; k0 += kChunk, ++accs) {
+          const uint32_t b = accs & 1u, d = tm0 + b * (uint32_t)kBN;
+          ok = tc::warp_wait_fast(&acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const int kb_end = min(nk, k0 + kChunk);
+          for (int kb = k0; kb < kb_end; ++kb) {
+            ok = tc::warp_wait_fast(&full[pos.slot], pos.phase, abort_flag);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t al = a0 + (uint32_t)pos.slot * (S::kABytes >> 4), bl = b0 + (uint32_t)pos.slot * (S::kBBytes >> 4);
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kBK / 16; ++k)
+                tc::mma_bf16_lo(d, al + 2u * k, bl + 2u * k, idesc, kb > k0 || k > 0 ? 1u : 0u);
+              tc::mma_commit(&empty[pos.slot]);
+              if (kb + 1 == kb_end) tc::mma_commit(&acc_full[b]);
+            }
+            __syncwarp();
+            pos.next();
+          }
+        }
+      }
+      if (!ok && lane == 0) {
         atomicOr(a.err, ZO_FLAG_TIMEOUT);
         *abort_flag = 1;
-        break;
       }
-      tc::tc_fence_after();
-      const uint32_t idesc = tc::idesc_bf16_f32(kBM, tile_units(t) * kUnit);
-      const uint32_t d = tmem + (uint32_t)(b * kBN);
-      for (int kb = 0; kb < nk; ++kb) {
-        const uint32_t s = consumed % kStages, ph = (consumed / kStages) & 1u;
-        if (*abort_flag || !tc::mbar_wait(&full[s], ph)) {
-          atomicOr(a.err, ZO_FLAG_TIMEOUT);
-          *abort_flag = 1;
-          break;
-        }
-        tc::tc_fence_after();
-        const uint32_t a0 = tc::smem_addr(sA + s * S::kABytes);
-        const uint32_t b0 = tc::smem_addr(sB + s * S::kBBytes);
-#pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          tc::mma_bf16(d, tc::smem_desc_k128(a0 + 32 * k), tc::smem_desc_k128(b0 + 32 * k), idesc,
-                       (kb | k) != 0 ? 1u : 0u);
-        tc::mma_commit(&empty[s]);
-        ++consumed;
-      }
-      if (*abort_flag) break;
-      tc::mma_commit(&acc_full[b]);
+      __syncwarp();
+      if (tc::elect_one()) tc::mma_commit(mma_done);  // arrives once every MMA above has retired
     }
-    tc::mma_commit(mma_done);  // arrives once every MMA issued above has retired
-  } else if (warp >= 2) {
-    const int q = warp & 3, quarter = (warp - 2) / 4;  // TMEM lane quadrant; quarter of the columns
+  } else {
+    tc::regs_inc<kMany>();
+    const int q = warp & 3, quarter = (warp - 4) / 4;  // TMEM lane quadrant; quarter of the columns
     const int row = m0 + 32 * q + lane;
     const int target = a.targets && row < a.rows ? a.targets[row] : -1;
     const bool any = m0 + 32 * q < a.rows;  // a warp without a row only passes the accumulators on
     RowStats st;
     bool ok = true;
-    for (int t = 0; t < tiles; ++t) {
-      const int b = t & 1;
-      if (!tc::warp_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u, abort_flag)) {
-        ok = false;
-        break;
+    uint32_t accs = 0;
+    for (int t = 0; ok && t < tiles; ++t) {
+      // this warp's columns of the tile
+      const int n0 = n_first + t * kBN + quarter * (kBN / 4), cols = min(kBN / 4, n_last - n0);
+      float x[64];
+      for (int k0 = 0; k0 < nk; k0 += kChunk, ++accs) {
+        const uint32_t b = accs & 1u;
+        if (!tc::warp_wait_fast(&acc_full[b], (accs >> 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        if (any && cols > 0)
+          add_columns(x, tmem + b * kBN + (uint32_t)(quarter * (kBN / 4)) + ((uint32_t)(q * 32) << 16), k0 == 0);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&acc_empty[b]);
       }
-      tc::tc_fence_after();
-      const int n0 = n_first + t * kBN, cols = min(kBN, n_last - n0);
-      const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
-      if (any) {
-#pragma unroll 1
-        for (int c0 = quarter * (kBN / 4); c0 < min(cols, (quarter + 1) * (kBN / 4)); c0 += 32)
-          take_chunk(st, base, n0, c0, cols, target, a.target_logit + row);
-      }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&acc_empty[b]);
+      if (ok && any && cols > 0) take_columns(st, x, n0, cols, target, a.target_logit + row);
     }
     if (!ok && lane == 0) {
       atomicOr(a.err, ZO_FLAG_TIMEOUT);
@@ -316,7 +353,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
   const uint32_t rank = tc::cluster_ctarank();
   const bool leader = rank == 0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int m0 = (int)blockIdx.x * kBM, split = blockIdx.y;  // blockIdx.x / 2 is the pair's row tile
   const int n_first = range_first(split, a.units, a.splits, kUnit);
   const int n_last = min(range_first(split + 1, a.units, a.splits, kUnit), a.vocab);
@@ -353,85 +390,97 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   };
 
   uint32_t issued = 0;
-  if (warp == 0 && lane == 0) {
-    tc::tma_prefetch_desc(&tmA);
-    tc::tma_prefetch_desc(&tmB);
-    for (int t = 0; t < tiles && !*abort_flag; ++t) {
-      const int boxes = tile_units(t);  // of each CTA: the tile's W rows split in the middle
-      const int b_row = n_first + t * kBN + (int)rank * boxes * kBox;
-      for (int kb = 0; kb < nk; ++kb) {
-        const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
-        if (*abort_flag || !tc::mbar_wait(&empty[s], ph ^ 1u)) {
-          raise_abort();
-          break;
+  if (warp < 4) {
+    tc::regs_dec<kFew>();
+    if (warp == 0 && lane == 0) {
+      tc::tma_prefetch_desc(&tmA);
+      tc::tma_prefetch_desc(&tmB);
+      for (int t = 0; t < tiles && !*abort_flag; ++t) {
+        const int boxes = tile_units(t);  // of each CTA: the tile's W rows split in the middle
+        const int b_row = n_first + t * kBN + (int)rank * boxes * kBox;
+        for (int kb = 0; kb < nk; ++kb) {
+          const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
+          if (*abort_flag || !tc::mbar_wait(&empty[s], ph ^ 1u)) {
+            raise_abort();
+            break;
+          }
+          if (leader) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::kABytes + (uint32_t)boxes * S::kBoxBytes));
+          tc::tma_load_2d_pair(sA + s * S::kABytes, &tmA, full_leader + 8u * s, kb * kBK, m0);
+          for (int b = 0; b < boxes; ++b)
+            tc::tma_load_2d_pair(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, full_leader + 8u * s, kb * kBK,
+                                 b_row + b * kBox);
+          ++issued;
         }
-        if (leader) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::kABytes + (uint32_t)boxes * S::kBoxBytes));
-        tc::tma_load_2d_pair(sA + s * S::kABytes, &tmA, full_leader + 8u * s, kb * kBK, m0);
-        for (int b = 0; b < boxes; ++b)
-          tc::tma_load_2d_pair(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, full_leader + 8u * s, kb * kBK,
-                               b_row + b * kBox);
-        ++issued;
       }
-    }
-    tc::pdl_launch_dependents();
-  } else if (warp == 1 && lane == 0 && leader) {
-    uint32_t consumed = 0;
-    for (int t = 0; t < tiles && !*abort_flag; ++t) {
-      const int b = t & 1;
-      if (!tc::mbar_wait(&acc_empty[b], ((uint32_t)(t >> 1) & 1u) ^ 1u)) {
-        raise_abort();
-        break;
-      }
-      tc::tc_fence_after();
-      const uint32_t idesc = tc::idesc_bf16_f32(2 * kBM, tile_units(t) * kUnit);
-      const uint32_t d = tmem + (uint32_t)(b * kBN);
-      for (int kb = 0; kb < nk; ++kb) {
-        const uint32_t s = consumed % kStages, ph = (consumed / kStages) & 1u;
-        if (*abort_flag || !tc::mbar_wait(&full[s], ph)) {
-          raise_abort();
-          break;
-        }
-        tc::tc_fence_after();
-        const uint32_t a0 = tc::smem_addr(sA + s * S::kABytes);
-        const uint32_t b0 = tc::smem_addr(sB + s * S::kBBytes);
+      tc::pdl_launch_dependents();
+    } else if (warp == 1 && leader) {  // MMAs: the warp in step, one lane issues
+      const uint32_t a0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sA), 0));
+      const uint32_t b0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sB), 0));
+      const uint32_t tm0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      tc::RingPos<kStages> pos;
+      uint32_t accs = 0;
+      bool ok = true;
+      for (int t = 0; ok && t < tiles; ++t) {
+        const uint32_t idesc = tc::idesc_bf16_f32(2 * kBM, tile_units(t) * kUnit);
+        for (int k0 = 0; ok && k0 < nk; k0 += kChunk, ++accs) {
+          const uint32_t b = accs & 1u, d = tm0 + b * (uint32_t)kBN;
+          ok = tc::warp_wait_fast(&acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const int kb_end = min(nk, k0 + kChunk);
+          for (int kb = k0; kb < kb_end; ++kb) {
+            ok = tc::warp_wait_fast(&full[pos.slot], pos.phase, abort_flag);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t al = a0 + (uint32_t)pos.slot * (S::kABytes >> 4), bl = b0 + (uint32_t)pos.slot * (S::kBBytes >> 4);
+            if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          tc::mma_bf16_pair(d, tc::smem_desc_k128(a0 + 32 * k), tc::smem_desc_k128(b0 + 32 * k), idesc,
-                            (kb | k) != 0 ? 1u : 0u);
-        tc::mma_commit_pair(&empty[s]);
-        ++consumed;
+              for (int k = 0; k < kBK / 16; ++k)
+                tc::mma_bf16_pair_lo(d, al + 2u * k, bl + 2u * k, idesc, kb > k0 || k > 0 ? 1u : 0u);
+              tc::mma_commit_pair(&empty[pos.slot]);
+              if (kb + 1 == kb_end) tc::mma_commit_pair(&acc_full[b]);
+            }
+            __syncwarp();
+            pos.next();
+          }
+        }
       }
-      if (*abort_flag) break;
-      tc::mma_commit_pair(&acc_full[b]);
+      if (!ok && lane == 0) raise_abort();
+      __syncwarp();
+      if (tc::elect_one()) tc::mma_commit_pair(mma_done);  // arrives (in both CTAs) once every MMA above has retired
     }
-    tc::mma_commit_pair(mma_done);  // arrives (in both CTAs) once every MMA above has retired
-  } else if (warp >= 2) {
-    const int q = warp & 3, quarter = (warp - 2) / 4;
+  } else {
+    tc::regs_inc<kMany>();
+    const int q = warp & 3, quarter = (warp - 4) / 4;
     const int row = m0 + 32 * q + lane;
     const int target = a.targets && row < a.rows ? a.targets[row] : -1;
     const bool any = m0 + 32 * q < a.rows;
     RowStats st;
-    for (int t = 0; t < tiles; ++t) {
-      const int b = t & 1;
-      if (!tc::warp_wait(&acc_full[b], (uint32_t)(t >> 1) & 1u, abort_flag)) {
-        if (lane == 0) raise_abort();
-        break;
+    bool ok = true;
+    uint32_t accs = 0;
+    for (int t = 0; ok && t < tiles; ++t) {
+      // this warp's columns of the tile
+      const int n0 = n_first + t * kBN + quarter * (kBN / 4), cols = min(kBN / 4, n_last - n0);
+      float x[64];
+      for (int k0 = 0; k0 < nk; k0 += kChunk, ++accs) {
+        const uint32_t b = accs & 1u;
+        if (!tc::warp_wait_fast(&acc_full[b], (accs >> 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        if (any && cols > 0)
+          add_columns(x, tmem + b * kBN + (uint32_t)(quarter * (kBN / 4)) + ((uint32_t)(q * 32) << 16), k0 == 0);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) tc::mbar_arrive(&acc_empty[b]);
+          else tc::mbar_arrive_remote(acc_empty_leader + 8u * b);
+        }
       }
-      tc::tc_fence_after();
-      const int n0 = n_first + t * kBN, cols = min(kBN, n_last - n0);
-      const uint32_t base = tmem + (uint32_t)(b * kBN) + ((uint32_t)(q * 32) << 16);
-      if (any) {
-#pragma unroll 1
-        for (int c0 = quarter * (kBN / 4); c0 < min(cols, (quarter + 1) * (kBN / 4)); c0 += 32)
-          take_chunk(st, base, n0, c0, cols, target, a.target_logit + row);
-      }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader) tc::mbar_arrive(&acc_empty[b]);
-        else tc::mbar_arrive_remote(acc_empty_leader + 8u * (uint32_t)b);
-      }
+      if (ok && any && cols > 0) take_columns(st, x, n0, cols, target, a.target_logit + row);
     }
+    if (!ok && lane == 0) raise_abort();
     stats[quarter * kBM + 32 * q + lane] = st;
   }
   tc::tc_fence_before();

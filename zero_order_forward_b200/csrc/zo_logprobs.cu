@@ -44,11 +44,7 @@ struct LogprobArgs {
   float *top_logprobs;
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
+using tc::max_nan;
 
 // Order of fp32 values as unsigned integers: NaN above +inf, -0 and +0 equal.
 __device__ __forceinline__ uint32_t order_of(float v) {

@@ -115,6 +115,13 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Two lanes of fp32 arithmetic per instruction (sm_100's packed f32x2 forms), each lane
 // rounded exactly as the scalar instruction: (d0, d1) = (a0 * b + c, a1 * b + c).
 __device__ __forceinline__ void fma2_bc(float a0, float a1, float b, float c, float &d0, float &d1) {
@@ -356,7 +363,10 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-// Descriptors by their low words: what changes from one MMA to the next is one addition.
+// For MMAs issued back to back: the issuing warp stays in step (its operands then lie in uniform
+// registers) and one elected lane issues; descriptors go by their low words, so that what changes
+// from one MMA to the next is one addition.  Built anew by a lane of its own in a branch they took
+// about 150 clocks each, more than an MMA of N = 128 runs.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version, 128-byte swizzle
 __device__ __forceinline__ uint32_t desc_k128_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_mn128_lo(uint32_t saddr, uint32_t lbo_bytes) {
@@ -573,6 +583,17 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t adesc, u
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16_pair_lo(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 
