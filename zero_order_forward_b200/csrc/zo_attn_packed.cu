@@ -104,21 +104,24 @@ __device__ __forceinline__ Item make_item(const PackedArgs &a, int row0, int len
   return it;
 }
 
-// Tiles of 2^shift rows of sequence i; 0 if it is empty or its offsets decrease or leave [0, total].
-__device__ __forceinline__ int seq_tiles(const PackedArgs &a, int i, int shift, bool &bad) {
-  bad = false;
-  if (i >= a.n_seqs) return 0;
+// A sequence's first row and length; no rows if its offsets decrease or leave [0, total].
+struct Seq {
+  int row0, len;
+  bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const PackedArgs &a, int i) {
+  if (i >= a.n_seqs) return {0, 0, false};
   const int s = __ldg(a.cu + i), e = __ldg(a.cu + i + 1);
-  bad = s < 0 || e < s || e > a.total;
-  return bad ? 0 : (int)(((uint32_t)(e - s) + (1u << shift) - 1u) >> shift);
+  const bool bad = s < 0 || e < s || e > a.total;
+  return {s, bad ? 0 : e - s, bad};
 }
 
 // The items of one CTA in their order (one warp).
 struct Schedule {
   const PackedArgs &a;
   int shift, group;        // log2 of a tile's rows; items of one tile (heads, or pairs of them)
-  int lane, first_tiles;   // this lane's count of the first 32 sequences, their rows
-  int first_row, first_len;
+  int lane;
+  Seq first;               // this lane's of the first 32 sequences
   int level, count;        // sequences with more than `level` tiles: `count`
   int64_t base, total;     // items of the longer levels; of all
   int longest;             // tiles of the longest sequence
@@ -128,30 +131,27 @@ struct Schedule {
     shift = a.mode == kRows ? 8 : 7;
     from = before = 0;
     group = a.mode == kRows ? a.H : a.H / 2;
-    first_row = lane < a.n_seqs ? __ldg(a.cu + lane) : 0;
-    first_len = lane < a.n_seqs ? __ldg(a.cu + lane + 1) - first_row : 0;
-    int most = 0, any_bad = 0;
-    int64_t tiles = 0;
-    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
-      bool bad;
-      const int n = seq_tiles(a, i0 + lane, shift, bad);
-      if (i0 == 0) first_tiles = n;
-      most = max(most, n);
-      tiles += n;
-      any_bad |= bad;
+    first = load_seq(a, lane);
+    int most = tiles_of(first), tiles = most;  // (fewer than 2^25 in all)
+    bool bad = first.bad;
+    for (int i0 = 32; i0 < a.n_seqs; i0 += 32) {
+      const Seq s = load_seq(a, i0 + lane);
+      most = max(most, tiles_of(s));
+      tiles += tiles_of(s);
+      bad |= s.bad;
     }
-    if (blockIdx.x == 0 && any_bad) atomicOr(a.err, ZO_FLAG_OFFSETS);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, o);
-    total = tiles * group;
+    if (blockIdx.x == 0 && bad) atomicOr(a.err, ZO_FLAG_OFFSETS);
+    total = (int64_t)__reduce_add_sync(0xFFFFFFFFu, tiles) * group;
     longest = __reduce_max_sync(0xFFFFFFFFu, most);
     level = longest - 1;
     base = 0;
     count = level >= 0 ? sequences() : 0;
   }
+  __device__ __forceinline__ int tiles_of(const Seq &s) const {
+    return (int)(((uint32_t)s.len + (1u << shift) - 1u) >> shift);
+  }
   __device__ __forceinline__ bool has(int i0) const {
-    bool bad;
-    return (i0 == 0 ? first_tiles : seq_tiles(a, i0 + lane, shift, bad)) > level;
+    return tiles_of(i0 == 0 ? first : load_seq(a, i0 + lane)) > level;
   }
   __device__ __forceinline__ int sequences() const {
     int n = 0;
@@ -175,7 +175,7 @@ struct Schedule {
       if (nth < before + __popc(in)) {
         const uint32_t lower = in & ((1u << lane) - 1u);
         const int i = from + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && before + __popc(lower) == nth)) - 1;
-        int row0 = __shfl_sync(0xFFFFFFFFu, first_row, i & 31), len = __shfl_sync(0xFFFFFFFFu, first_len, i & 31);
+        int row0 = __shfl_sync(0xFFFFFFFFu, first.row0, i & 31), len = __shfl_sync(0xFFFFFFFFu, first.len, i & 31);
         if (from > 0) {
           row0 = __ldg(a.cu + i);
           len = __ldg(a.cu + i + 1) - row0;
