@@ -27,8 +27,7 @@
 //     (repair_rows) and recomputed from its own keys alone where a later row is to blame.
 #include <cmath>
 
-#include "zo_internal.cuh"
-#include "zo_tc.cuh"
+#include "zo_attn_packed.cuh"
 
 namespace zo {
 namespace {
@@ -45,6 +44,12 @@ constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kBox = kM * 128;    // bytes of one 128-row x 64-column bf16 box
 constexpr int kItems = 2;              // items on hand
 
+// Sequences of at most kShortSeq tokens go to a kernel of their own where the mean length (the buffer's
+// over their number; lengths are known on the device only) lets there be many of them.  16 heads of
+// 128: 64 sequences of 16 tokens take 7.8 us instead of 16.4, 64 of 32 9.7 instead of 17; 64 of 64, of
+// which it finds none, 20.4 instead of 18.7, and sequences of some thousand tokens as much more.
+constexpr int kShortMean = 256;
+
 enum Mode { kHeads, kPair64, kRows };
 
 template <int HD, bool SPLIT>  // SPLIT: the streams have key/value heads of their own (kPair64)
@@ -59,17 +64,6 @@ struct PackedSmem {
   static constexpr uint32_t kItem = kBar + 8 * ((kNumBars + 2) / 2 * 2);   // Item [kItems]
   static constexpr uint32_t kBytes = kItem + kItems * 48 + 1024;           // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory");
-};
-
-struct PackedArgs {
-  const uint16_t *q, *k, *v;
-  uint16_t *out;
-  const int32_t *cu;
-  int n_seqs, total, H, Hk;
-  int64_t ldq, ldk, ldv, ldo;
-  float scale_log2;
-  int mode, shared;  // query heads of a key/value head
-  uint32_t *err;
 };
 
 // What the two streams of an item do.
@@ -104,18 +98,6 @@ __device__ __forceinline__ Item make_item(const PackedArgs &a, int row0, int len
   return it;
 }
 
-// A sequence's first row and length; no rows if its offsets decrease or leave [0, total].
-struct Seq {
-  int row0, len;
-  bool bad;
-};
-__device__ __forceinline__ Seq load_seq(const PackedArgs &a, int i) {
-  if (i >= a.n_seqs) return {0, 0, false};
-  const int s = __ldg(a.cu + i), e = __ldg(a.cu + i + 1);
-  const bool bad = s < 0 || e < s || e > a.total;
-  return {s, bad ? 0 : e - s, bad};
-}
-
 // The items of one CTA in their order (one warp).
 struct Schedule {
   const PackedArgs &a;
@@ -148,7 +130,7 @@ struct Schedule {
     count = level >= 0 ? sequences() : 0;
   }
   __device__ __forceinline__ int tiles_of(const Seq &s) const {
-    return (int)(((uint32_t)s.len + (1u << shift) - 1u) >> shift);
+    return s.len <= a.handled ? 0 : (int)(((uint32_t)s.len + (1u << shift) - 1u) >> shift);
   }
   __device__ __forceinline__ bool has(int i0) const {
     return tiles_of(i0 == 0 ? first : load_seq(a, i0 + lane)) > level;
@@ -188,71 +170,6 @@ struct Schedule {
     return it;
   }
 };
-
-__device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
-
-// Rows first + (bits of `rows`) of the tile came out infinite or NaN.  That is right if a value
-// row that they attend to says so; it is wrong where only a later row of the tile's last keys
-// (up to key_end) does.  One warp: a row with a non-finite later value row, and with a non-finite
-// output that no own key's value explains, is computed again from keys 0 .. r alone, in fp32.
-template <int HD>
-__device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len, int first, uint32_t rows,
-                                         int h, int kvh, int key_end) {
-  constexpr int C = HD / 32;  // output columns of a lane: C lane .. C lane + C - 1
-  const int lane = threadIdx.x & 31;
-  const uint16_t *K = a.k + (int64_t)row0 * a.ldk + kvh * HD;
-  const uint16_t *V = a.v + (int64_t)row0 * a.ldv + kvh * HD + C * lane;
-  for (; rows; rows &= rows - 1) {
-    const int r = first + __ffs(rows) - 1;
-    bool later = false;
-    for (int j = r + 1; j < min(key_end, len); ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c) later |= !finite_bf16(V[(int64_t)j * a.ldv + c]);
-    if (!__any_sync(0xFFFFFFFFu, later)) continue;
-    uint16_t *orow = a.out + (int64_t)(row0 + r) * a.ldo + h * HD + C * lane;
-    uint32_t open = 0;  // this lane's non-finite outputs not explained yet
-#pragma unroll
-    for (int c = 0; c < C; ++c) open |= finite_bf16(orow[c]) ? 0u : 1u << c;
-    for (int j = 0; j <= r && __any_sync(0xFFFFFFFFu, open); ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (!finite_bf16(V[(int64_t)j * a.ldv + c])) open &= ~(1u << c);
-    if (!__any_sync(0xFFFFFFFFu, open)) continue;
-    const uint16_t *q = a.q + (int64_t)(row0 + r) * a.ldq + h * HD;
-    float m = -INFINITY, l = 0.f, acc[C] = {};
-    for (int j0 = 0; j0 <= r; j0 += 32) {
-      const int j = j0 + lane;
-      float s = -INFINITY;
-      if (j <= r) {
-        s = 0.f;
-        for (int e = 0; e < HD; ++e)
-          s = fmaf(bf16_bits_to_f32(q[e]), bf16_bits_to_f32(K[(int64_t)j * a.ldk + e]), s);
-        s *= a.scale_log2;
-      }
-      float mx = s;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-      mx = fmaxf(mx, m);
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      const float f = ex2(m - ref), p = j <= r ? ex2(s - ref) : 0.f;
-      float sum = p;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      l = l * f + sum;
-      m = mx;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] *= f;
-      for (int t = 0; t < 32 && j0 + t <= r; ++t) {
-        const float pt = __shfl_sync(0xFFFFFFFFu, p, t);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          acc[c] = fmaf(pt, bf16_bits_to_f32(V[(int64_t)(j0 + t) * a.ldv + c]), acc[c]);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) orow[c] = f32_to_bf16_bits(acc[c] / l);
-  }
-}
 
 // One row's step over the first 32 NC keys of a tile: its scores from tensor memory at tS, maximum,
 // probabilities back to the first 16 NC columns there, sum.  MASK: keys behind `last` do not count
@@ -319,23 +236,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
   }
   l += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
   tc::tmem_st_wait();
-}
-
-// The words a[0 .. 3] of a quad's lanes transposed: a[k] becomes lane k's word of this lane's number.
-__device__ __forceinline__ void quad_transpose(uint32_t (&a)[4]) {
-  const int c = threadIdx.x & 3;
-#pragma unroll
-  for (int k = 0; k < 4; k += 2) {
-    const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, c & 1 ? a[k] : a[k + 1], 1);
-    if (c & 1) a[k] = v;
-    else a[k + 1] = v;
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, c & 2 ? a[k] : a[k + 2], 2);
-    if (c & 2) a[k] = v;
-    else a[k + 2] = v;
-  }
 }
 
 template <int HD, bool SPLIT>
@@ -722,10 +622,15 @@ extern "C" zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void 
     return fail(ctx, ZO_ERR_CUDA, "attention_packed: cuTensorMapEncodeTiled failed");
   const int shared = n_heads / n_kv_heads;
   const Mode mode = shared % 2 == 0 ? kHeads : head_dim == 64 && shared == 1 && n_heads % 2 == 0 ? kPair64 : kRows;
-  const PackedArgs a{static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
+  PackedArgs a{static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
                      static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out), cu_seqlens, n_seqs,
                      (int)total_tokens, n_heads, n_kv_heads, ldq, ldk, ldv, ldo,
-                     scale * 1.4426950408889634f, (int)mode, shared, &ctx->dstate->flags};
+                     scale * 1.4426950408889634f, (int)mode, shared, 0, &ctx->dstate->flags};
+  if (total_tokens / n_seqs <= kShortMean) {
+    const zo_status st = launch_attn_short(ctx, a, head_dim);
+    if (st != ZO_OK || total_tokens <= kShortSeq) return st;
+    a.handled = kShortSeq;
+  }
   if (head_dim == 128) return launch<128, false>(ctx, tmq, tmk, tmv, a);
   return mode == kPair64 ? launch<64, true>(ctx, tmq, tmk, tmv, a) : launch<64, false>(ctx, tmq, tmk, tmv, a);
 }
