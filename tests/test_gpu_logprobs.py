@@ -138,7 +138,7 @@ def test_largest_logits_crowded_into_few_places(zo, ctx, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("n,rows", [(20000, 200), (3000, 160), (700, 30)])
+@pytest.mark.parametrize("n,rows", [(20000, 200), (3000, 160), (700, 30), (700, 4100), (3000, 4003), (9000, 900)])
 def test_ties_masks_and_bad_rows_where_a_block_has_a_row_of_its_own(zo, ctx, dtype, n, rows):
     """The same kinds of rows with enough of them that none is split, and with rows of one warp."""
     g = torch.Generator(device="cuda").manual_seed(n)
@@ -150,7 +150,7 @@ def test_ties_masks_and_bad_rows_where_a_block_has_a_row_of_its_own(zo, ctx, dty
              torch.full((n,), low, device="cuda"), torch.where((at // 8) % 128 < 9, 10.0 + (at % 7).float(), 0.0)]
     x = torch.stack([kinds[i % len(kinds)] for i in range(rows)]).to(TYPES[dtype])
     t = torch.full((rows,), n - 1, dtype=torch.int32, device="cuda")
-    for top in (5, 32):
+    for top in (5, 20, 32):
         check(x, t, call(zo, ctx, x, t, top), top)
     x[3, n // 2] = math.nan
     x[11, 0] = math.inf

@@ -563,10 +563,14 @@ cudaError_t launch(LogprobArgs &a, int64_t rows, cudaStream_t st) {
   a.splits = 1;
   // several blocks a row while that leaves SMs to fill and every thread has a vector
   while (a.splits < kMaxSplits && rows * a.splits <= kSmCount && vectors >= 2 * a.splits * 256) a.splits *= 2;
-  // Few threads hold more logits each above the bound than it has to let through.
-  if (vectors >= 1024) return launch_one<T, 256>(a, rows, st);
-  if (vectors >= 256 || a.top > 8) return launch_one<T, 128>(a, rows, st);
-  return launch_one<T, 32>(a, rows, st);
+  // As few threads a row as still fill the SMs with loads (148 x 32 warps fit): a row's joins and
+  // selection cost about the same on a warp as on 8, which also wait for one another, but a warp's bound
+  // lets more candidates of a long row through.  bf16, 5 alternatives, on 32 / 128 / 256 threads:
+  // 12000 x 4000 42 / 78 / 129 us, 1000 x 4000 12 / 8.2 / 12, 30 x 20000 9.9 / 9.5 / 7.1; fp32, 20
+  // alternatives, 509 x 49999: 128 threads 38, 256 25.
+  if (rows >= 4000 && vectors < 2048) return launch_one<T, 32>(a, rows, st);
+  if (rows >= 6 * kSmCount || vectors < 1024) return launch_one<T, 128>(a, rows, st);
+  return launch_one<T, 256>(a, rows, st);
 }
 
 }  // namespace
