@@ -35,10 +35,9 @@ constexpr int kThreads = 32 * (4 + kEpiWarps);  // loads, MMAs, two idle ones; e
 constexpr int kFew = 32, kMany = 112;
 // The tensor cores truncate each addition to an fp32 accumulator: over a width of 2048 the entropy
 // came out off by 1.1e-6 and over 4096 by 2.1e-6, where rounded sums give 1e-7 to 9e-7.  So an
-// accumulator takes this many 64-wide steps, and the epilogue adds accumulators up, rounded: 16
-// steps leave 6e-7 and 1.3e-6 and cost 1% of the time at a width of 2048, 8 would leave 3e-7 and 6e-7
-// and cost 3.5%.
-constexpr int kChunk = 16;
+// accumulator takes a part of the width, and the epilogue adds accumulators up, rounded: 1024 leave
+// 6e-7 at a width of 2048 and 1.7e-6 at 4096 and cost 1% of the time, 512 leave 3e-7 and 8e-7 and cost 3.5%.
+__host__ __device__ constexpr int chunk_steps(int width) { return width <= 2048 ? 16 : 8; }  // of 64
 
 template <bool PAIR>
 struct HeadCfg {
@@ -60,7 +59,7 @@ struct HeadArgs {
   int units;              // of W's rows
   int a_rows;             // rows of a box of `hidden` (a multiple of 8; those behind are not loaded)
   const int32_t *targets; // may be null
-  float4 *part;           // [rows][splits] (m, s, u, -)
+  float4 *part;           // [rows][splits] (m, s, u, what s lost to rounding)
   float *target_logit;    // [rows]
   uint32_t *err;
 };
@@ -134,7 +133,7 @@ __device__ __forceinline__ void write_part(const HeadArgs &a, const RowStats *qu
   for (int k = 0; k < kEpiWarps / 4; ++k) r.m = fmaxf(r.m, quarter[k * kBM].m);
 #pragma unroll
   for (int k = 0; k < kEpiWarps / 4; ++k) quarter[k * kBM].add_to(r.m, r.s, r.u);
-  a.part[(int64_t)row * a.splits + split] = make_float4(r.m, (float)r.s, (float)r.u, 0.f);
+  a.part[(int64_t)row * a.splits + split] = make_float4(r.m, (float)r.s, (float)r.u, (float)(r.s - (double)(float)r.s));
 }
 
 // What an epilogue thread does with one accumulator: its row's 64 columns from taddr on, added to x.
@@ -192,7 +191,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   const int n_first = range_first(split, a.units, a.splits, kUnit);
   const int n_last = min(range_first(split + 1, a.units, a.splits, kUnit), a.vocab);
   const int tiles = (n_last - n_first + kBN - 1) / kBN;
-  const int nk = (a.width + kBK - 1) / kBK;
+  const int nk = (a.width + kBK - 1) / kBK, chunk = chunk_steps(a.width);
   // loaded rows of a tile: whole units (rows past the vocabulary read as zero and are masked)
   auto tile_units = [&](int t) { return min(kBN / kUnit, (n_last - n_first - t * kBN + kUnit - 1) / kUnit); };
 
@@ -249,12 +248,12 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       bool ok = true;
       for (int t = 0; ok && t < tiles; ++t) {
         const uint32_t idesc = tc::idesc_bf16_f32(kBM, tile_units(t) * kUnit);
-        for (int k0 = 0; ok && k0 < nk; k0 += kChunk, ++accs) {
+        for (int k0 = 0; ok && k0 < nk; k0 += chunk, ++accs) {
           const uint32_t b = accs & 1u, d = tm0 + b * (uint32_t)kBN;
           ok = tc::warp_wait_fast(&acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           tc::tc_fence_after();
-          const int kb_end = min(nk, k0 + kChunk);
+          const int kb_end = min(nk, k0 + chunk);
           for (int kb = k0; kb < kb_end; ++kb) {
             ok = tc::warp_wait_fast(&full[pos.slot], pos.phase, abort_flag);
             if (!ok) break;
@@ -292,7 +291,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       // this warp's columns of the tile
       const int n0 = n_first + t * kBN + quarter * (kBN / 4), cols = min(kBN / 4, n_last - n0);
       float x[64];
-      for (int k0 = 0; k0 < nk; k0 += kChunk, ++accs) {
+      for (int k0 = 0; k0 < nk; k0 += chunk, ++accs) {
         const uint32_t b = accs & 1u;
         if (!tc::warp_wait_fast(&acc_full[b], (accs >> 1) & 1u, abort_flag)) {
           ok = false;
@@ -358,7 +357,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   const int n_first = range_first(split, a.units, a.splits, kUnit);
   const int n_last = min(range_first(split + 1, a.units, a.splits, kUnit), a.vocab);
   const int tiles = (n_last - n_first + kBN - 1) / kBN;
-  const int nk = (a.width + kBK - 1) / kBK;
+  const int nk = (a.width + kBK - 1) / kBK, chunk = chunk_steps(a.width);
   auto tile_units = [&](int t) { return min(kBN / kUnit, (n_last - n_first - t * kBN + kUnit - 1) / kUnit); };
 
   if (threadIdx.x == 0) {
@@ -422,12 +421,12 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       bool ok = true;
       for (int t = 0; ok && t < tiles; ++t) {
         const uint32_t idesc = tc::idesc_bf16_f32(2 * kBM, tile_units(t) * kUnit);
-        for (int k0 = 0; ok && k0 < nk; k0 += kChunk, ++accs) {
+        for (int k0 = 0; ok && k0 < nk; k0 += chunk, ++accs) {
           const uint32_t b = accs & 1u, d = tm0 + b * (uint32_t)kBN;
           ok = tc::warp_wait_fast(&acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           tc::tc_fence_after();
-          const int kb_end = min(nk, k0 + kChunk);
+          const int kb_end = min(nk, k0 + chunk);
           for (int kb = k0; kb < kb_end; ++kb) {
             ok = tc::warp_wait_fast(&full[pos.slot], pos.phase, abort_flag);
             if (!ok) break;
@@ -462,7 +461,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       // this warp's columns of the tile
       const int n0 = n_first + t * kBN + quarter * (kBN / 4), cols = min(kBN / 4, n_last - n0);
       float x[64];
-      for (int k0 = 0; k0 < nk; k0 += kChunk, ++accs) {
+      for (int k0 = 0; k0 < nk; k0 += chunk, ++accs) {
         const uint32_t b = accs & 1u;
         if (!tc::warp_wait_fast(&acc_full[b], (accs >> 1) & 1u, abort_flag)) {
           ok = false;
@@ -535,7 +534,7 @@ head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
   for (int k = 0; k < N; ++k) {
     RowStats r;
     r.m = t[k].x;
-    r.s = (double)t[k].y;
+    r.s = (double)t[k].y + (double)t[k].w;
     r.u = (double)t[k].z;
     r.add_to(m, s, u);
   }

@@ -6,8 +6,8 @@
 // A row is one block's, or, where rows are few, a cluster's of up to 8 blocks.  Every thread keeps,
 // over the 16-byte vectors that it reads, m (its largest logit so far), s = sum 2^t and
 // u = sum 2^t t with t = (x - m) log2 e; a larger maximum rescales both.  The triples are joined
-// in a fixed order, so that H = ln 2 (log2 s - u / s) and logprob = (x_t - m) - ln 2 log2 s; the
-// logarithm and the last sums are fp64, once per row.  The difference x - m is taken before the
+// in a fixed order, so that H = ln 2 (log2 s - u / s) and logprob = (x_t - m) - ln 2 log2 s; sums
+// beyond a few vectors' and the logarithm are fp64.  The difference x - m is taken before the
 // scaling, so that rows of huge logits lose and overflow nothing.
 //
 // Alternatives: a thread also keeps which of its vectors holds its largest logit first.  The
@@ -107,8 +107,11 @@ template <> struct Row<uint16_t> {
   }
 };
 
+// Sums in fp64: where one token has nearly all the probability, s is 1 and a little, and the little is
+// the entropy; fp32 joins left it off by 2e-6.
 struct Stats {
-  float m, s, u;  // see above; m = -inf: nothing yet (s = u = 0)
+  float m;      // see above; m = -inf: nothing yet (s = u = 0)
+  double s, u;
 };
 
 // The lanes' triples joined, in every lane: the sums relative to the largest m, then added in a
@@ -121,8 +124,8 @@ __device__ __forceinline__ void warp_join(Stats &t, float &top) {
     top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   }
   const float d = fmaxf((t.m - m) * kLog2E, -kLowest), f = tc::ex2(d);  // (-inf) - (-inf): -kLowest
-  t.u = f > 0.f ? f * fmaf(d, t.s, t.u) : 0.f;
-  t.s *= f;
+  t.u = f > 0.f ? (double)f * (t.u + (double)d * t.s) : 0.0;
+  t.s *= (double)f;
   t.m = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -223,7 +226,8 @@ struct Scan {
   static constexpr int V = Row<T>::kVec;
   float top = -INFINITY;  // its largest logit (NaN once it has seen one)
   int top_vec;            // the first vector that holds it
-  float m = -INFINITY, s[4] = {}, u[4] = {};
+  float m = -INFINITY, u = 0.f;  // (u has no term of the largest logit that the others would vanish beside)
+  double s = 0.0;
 
   template <int U>
   __device__ __forceinline__ float take(const uint4 (&r)[U], int j, int step) {  // returns the largest
@@ -241,14 +245,12 @@ struct Scan {
     if (top > m) {
       if (m != -INFINITY) {
         const float d = fmaxf((m - top) * kLog2E, -kLowest), e = tc::ex2(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[i] = e * fmaf(d, s[i], u[i]);
-          s[i] *= e;
-        }
+        u = e * (u + d * (float)s);
+        s *= (double)e;
       }
       m = top;
     }
+    float s4[4] = {}, u4[4] = {};  // of these U vectors, in four chains
 #pragma unroll
     for (int g = 0; g < U; ++g) {
       float f[V];
@@ -262,14 +264,13 @@ struct Scan {
         const float p0 = tc::ex2(t0), p1 = tc::ex2(t1);
         constexpr int kPairs = 2;
         const int h = (i / 2) % kPairs * 2;
-        tc::add2(s[h], s[h + 1], p0, p1);
-        tc::fma2(u[h], u[h + 1], p0, p1, t0, t1);
+        tc::add2(s4[h], s4[h + 1], p0, p1);
+        tc::fma2(u4[h], u4[h + 1], p0, p1, t0, t1);
       }
     }
+    s += (double)((s4[0] + s4[1]) + (s4[2] + s4[3]));
+    u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
     return all;
-  }
-  __device__ __forceinline__ Stats stats() const {
-    return {m, (s[0] + s[1]) + (s[2] + s[3]), (u[0] + u[1]) + (u[2] + u[3])};
   }
 };
 
@@ -379,7 +380,7 @@ logprobs_kernel(const LogprobArgs a) {
 
   // ---- the statistics of the block's part
   float top = scan.top;
-  Stats st = scan.stats();
+  Stats st{scan.m, scan.s, (double)scan.u};
   warp_join(st, top);
   if (lane == 0) {
     sh.warp_stats[warp] = st;
@@ -483,7 +484,7 @@ logprobs_kernel(const LogprobArgs a) {
   // ---- the row: its parts' statistics and alternatives meet in block 0
   if (warp == 0) {
     if (WARPS > 1) {
-      st = lane < WARPS ? sh.warp_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+      st = lane < WARPS ? sh.warp_stats[lane] : Stats{-INFINITY, 0.0, 0.0};
       top = lane < WARPS ? sh.warp_top[lane] : -INFINITY;
       warp_join(st, top);
     }
@@ -511,7 +512,7 @@ logprobs_kernel(const LogprobArgs a) {
       }
     }
     if (warp != 0) return;
-    st = lane < a.splits ? sh.row_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+    st = lane < a.splits ? sh.row_stats[lane] : Stats{-INFINITY, 0.0, 0.0};
     top = lane < a.splits ? sh.row_top[lane] : -INFINITY;
     warp_join(st, top);
   } else {
@@ -521,10 +522,10 @@ logprobs_kernel(const LogprobArgs a) {
   top = __shfl_sync(0xFFFFFFFFu, top, 0);
   const bool none = !(top > -INFINITY) || top == INFINITY;
   const double nan = __longlong_as_double(0x7FF8000000000000ll);
-  const double log2s = none ? nan : log2((double)__shfl_sync(0xFFFFFFFFu, st.s, 0));
+  const double log2s = none ? nan : log2(__shfl_sync(0xFFFFFFFFu, st.s, 0));
   const double big = (double)__shfl_sync(0xFFFFFFFFu, st.m, 0);
   if (lane == 0) {
-    if (a.entropy) a.entropy[r] = (float)(kLn2 * (log2s - (double)st.u / (double)st.s));
+    if (a.entropy) a.entropy[r] = (float)(kLn2 * (log2s - st.u / st.s));
     if (a.logprob) {
       float v = (float)nan;
       if (target == -1) v = 0.f;
