@@ -331,10 +331,13 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   }
 }
 
-// The CTA-pair form: the roles of head_kernel, with the leader (CTA 0) issuing the MMAs of both and
+// The CTA-pair form (tmW: a whole tile's rows of W in one box.  Four boxes of 32 rows a stage, which the
+// last tile of a range still takes, held the tensor pipe at 63%: 4096 x 151936 x 2048 took 1950 us, with
+// whole boxes 1648): the roles of head_kernel, with the leader (CTA 0) issuing the MMAs of both and
 // each CTA's epilogue warps reading the 128 rows of its own tensor memory.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, HeadArgs a) {
+head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmW, HeadArgs a) {
   using S = HeadCfg<true>;
   constexpr int kStages = S::kStages, kUnit = S::kUnit;
   extern __shared__ uint8_t smem_raw[];
@@ -394,6 +397,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (warp == 0 && lane == 0) {
       tc::tma_prefetch_desc(&tmA);
       tc::tma_prefetch_desc(&tmB);
+      tc::tma_prefetch_desc(&tmW);
       for (int t = 0; t < tiles && !*abort_flag; ++t) {
         const int boxes = tile_units(t);  // of each CTA: the tile's W rows split in the middle
         const int b_row = n_first + t * kBN + (int)rank * boxes * kBox;
@@ -405,7 +409,9 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           }
           if (leader) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::kABytes + (uint32_t)boxes * S::kBoxBytes));
           tc::tma_load_2d_pair(sA + s * S::kABytes, &tmA, full_leader + 8u * s, kb * kBK, m0);
-          for (int b = 0; b < boxes; ++b)
+          if (boxes == kBN / 2 / kBox)
+            tc::tma_load_2d_pair(sB + s * S::kBBytes, &tmW, full_leader + 8u * s, kb * kBK, b_row);
+          else for (int b = 0; b < boxes; ++b)
             tc::tma_load_2d_pair(sB + s * S::kBBytes + b * S::kBoxBytes, &tmB, full_leader + 8u * s, kb * kBK,
                                  b_row + b * kBox);
           ++issued;
@@ -651,16 +657,18 @@ zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64
   a.part = static_cast<float4 *>(workspace);
   a.target_logit = reinterpret_cast<float *>(a.part + rows * a.splits);
   a.err = &ctx->dstate->flags;
-  CUtensorMap ta, tb;
-  if (!tile_map_bf16(&ta, hidden, rows, width, ldh, a.a_rows) || !tile_map_bf16(&tb, W, vocab, width, ldw, kBox))
+  CUtensorMap ta, tb, tw;
+  if (!tile_map_bf16(&ta, hidden, rows, width, ldh, a.a_rows) || !tile_map_bf16(&tb, W, vocab, width, ldw, kBox) ||
+      (pairs && !tile_map_bf16(&tw, W, vocab, width, ldw, kBN / 2)))
     return fail(ctx, ZO_ERR_CUDA, "head_logprobs: cuTensorMapEncodeTiled failed");
-  auto kernel = pairs ? head_pair_kernel : head_kernel;
+  const void *kernel = pairs ? reinterpret_cast<const void *>(head_pair_kernel) : reinterpret_cast<const void *>(head_kernel);
   const int smem = (int)(pairs ? HeadCfg<true>::kBytes : HeadCfg<false>::kBytes);
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
+  cudaError_t e = ensure_smem_limit(kernel, smem);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_kernel attribute: %s", cudaGetErrorString(e));
   const int64_t m = (rows + kBM - 1) / kBM;
   const dim3 grid((unsigned)(pairs ? (m + 1) / 2 * 2 : m), (unsigned)a.splits);
-  e = launch_early(kernel, grid, kThreads, smem, ctx->stream, ta, tb, a);
+  e = pairs ? launch_early(head_pair_kernel, grid, kThreads, smem, ctx->stream, ta, tb, tw, a)
+            : launch_early(head_kernel, grid, kThreads, smem, ctx->stream, ta, tb, a);
   if (e != cudaSuccess) return fail(ctx, ZO_ERR_CUDA, "head_kernel: %s", cudaGetErrorString(e));
   ctx->launches += 1;
   e = launch_early(head_join_kernel, dim3((unsigned)((rows + 7) / 8)), 256, 0, ctx->stream, a, logprob, entropy);
