@@ -7,10 +7,10 @@
 // computed in fp64 on the host and travel as a kernel parameter.
 //
 // A group of threads covers one head, 16 bytes of each half (half layout) or 16 bytes (interleaved) a
-// thread, and takes kHeads heads of one row: their loads are under way before the thread computes
+// thread, and takes HEADS (4 or 8) heads of one row: their loads are under way before the thread computes
 // the cosines and sines of its own pairs, once for those heads: position x (f_i / 2 pi) in fp64, the
 // fraction of a turn kept (exact enough at any int32 position: the product carries 53 bits, at most
-// 31 of them before the point), then sincospi in fp32.  Computing them again for every kHeads heads
+// 31 of them before the point), then sincospi in fp32.  Computing them again for every HEADS heads
 // costs less than a block that computes them once, waits and shares them: 8192 rows of 24 heads of
 // 128 took 22.3 us that way.
 // Bound: HBM, two passes over the rotated heads.
@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = ZO_ROPE_MAX_HEAD_DIM / 2;
-constexpr int kHeads = 4;  // heads of a group of threads
 
 struct RopeArgs {
   const void *x;
@@ -83,7 +82,7 @@ template <typename T> struct Pack<T, 1> {
 // VEC: elements of one access (16 bytes' worth, or 1 where a pointer, a stride or a dimension is
 // not a multiple of 16 bytes).  A rotating unit of the half layout covers VEC pairs with one
 // access in each half; of the interleaved layout VEC / 2 pairs (VEC = 1: one pair, two accesses).
-template <typename T, bool IL, int VEC>
+template <typename T, bool IL, int VEC, int HEADS>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeArgs a) {
   using P = Pack<T, VEC>;
@@ -96,7 +95,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   const int groups = kRopeThreads / a.units;
   const int64_t row = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * groups + group;
   if (group >= groups || row >= a.rows) return;
-  const int head0 = blockIdx.x * kHeads, heads = min(kHeads, a.heads - head0);
+  const int head0 = blockIdx.x * HEADS, heads = min(HEADS, a.heads - head0);
   const bool turns = unit < a.rot_units;  // the other units copy features behind rot_dim
   // the unit's first access, and its second in the rotating part
   const int fa = !turns ? 2 * a.pairs + (unit - a.rot_units) * VEC : IL && VEC == 1 ? 2 * unit : unit * VEC;
@@ -104,9 +103,9 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   const T *xi = static_cast<const T *>(a.x) + row * a.ldx + (int64_t)head0 * a.head_dim;
   T *oi = static_cast<T *>(a.out) + row * a.ldo + (int64_t)head0 * a.head_dim;
   const double pos = a.positions ? (double)a.positions[row] : (double)row;
-  Raw first[kHeads], second[kHeads];
+  Raw first[HEADS], second[HEADS];
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
+  for (int h = 0; h < HEADS; ++h) {
     if (h < heads) {
       first[h] = *reinterpret_cast<const Raw *>(xi + h * a.head_dim + fa);
       if (!kOne && turns) second[h] = *reinterpret_cast<const Raw *>(xi + h * a.head_dim + fb);
@@ -114,7 +113,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   }
   if (!turns) {
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
+    for (int h = 0; h < HEADS; ++h)
       if (h < heads) *reinterpret_cast<Raw *>(oi + h * a.head_dim + fa) = first[h];
     return;
   }
@@ -127,7 +126,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
     s[i] *= a.magnitude;
   }
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
+  for (int h = 0; h < HEADS; ++h) {
     if (h < heads) {
       float u[VEC], v[VEC];
       P::open(first[h], u);
@@ -153,6 +152,14 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   }
 }
 
+template <typename T, bool IL, int VEC, int HEADS>
+cudaError_t run(const RopeArgs &a, cudaStream_t st) {
+  const int64_t groups = kRopeThreads / a.units, blocks = (a.rows + groups - 1) / groups;
+  const int64_t y = blocks < 65535 ? blocks : 65535;  // row blocks over y and z
+  const dim3 grid((unsigned)((a.heads + HEADS - 1) / HEADS), (unsigned)y, (unsigned)((blocks + y - 1) / y));
+  return launch_early(rope_kernel<T, IL, VEC, HEADS>, grid, kRopeThreads, 0, st, a);
+}
+
 template <typename T>
 cudaError_t launch(RopeArgs &a, bool interleaved, bool in_place, cudaStream_t st) {
   constexpr int kVec = Elem<T>::kVec;
@@ -165,15 +172,16 @@ cudaError_t launch(RopeArgs &a, bool interleaved, bool in_place, cudaStream_t st
   const int vec = wide ? kVec : 1;
   a.rot_units = interleaved && wide ? 2 * a.pairs / vec : a.pairs / vec;
   a.units = a.rot_units + (in_place ? 0 : rest / vec);
-  const int64_t groups = kRopeThreads / a.units, blocks = (a.rows + groups - 1) / groups;
-  // row blocks over y and z
-  const int64_t y = blocks < 65535 ? blocks : 65535;
-  const dim3 grid((unsigned)((a.heads + kHeads - 1) / kHeads), (unsigned)y, (unsigned)((blocks + y - 1) / y));
-  if (interleaved)
-    return wide ? launch_early(rope_kernel<T, true, kVec>, grid, kRopeThreads, 0, st, a)
-                : launch_early(rope_kernel<T, true, 1>, grid, kRopeThreads, 0, st, a);
-  return wide ? launch_early(rope_kernel<T, false, kVec>, grid, kRopeThreads, 0, st, a)
-              : launch_early(rope_kernel<T, false, 1>, grid, kRopeThreads, 0, st, a);
+  // Heads of a group: 4 keep most loads in flight, 8 share the angles among more.  4 / 8, us: 8192 rows of
+  // 24 heads of 128 17.3 / 17.7, 30000 of 2 of 256 19.1 / 22.6, but 29710 of 6 of 128 fp32 38 / 28.5, and
+  // element by element 8192 of 24 of 128 50 / 41.
+  const bool more = a.heads > 4 && (a.heads <= 8 || !wide);
+  if (interleaved) {
+    if (wide) return more ? run<T, true, kVec, 8>(a, st) : run<T, true, kVec, 4>(a, st);
+    return more ? run<T, true, 1, 8>(a, st) : run<T, true, 1, 4>(a, st);
+  }
+  if (wide) return more ? run<T, false, kVec, 8>(a, st) : run<T, false, kVec, 4>(a, st);
+  return more ? run<T, false, 1, 8>(a, st) : run<T, false, 1, 4>(a, st);
 }
 
 // Why `c` is not a rotary configuration, or null.
