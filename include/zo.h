@@ -698,9 +698,9 @@ zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void *k, const v
  *   top_ids (int32), top_logprobs (fp32)  device [rows][top]; either may be NULL, top = 0: none.
  * A logit of -inf rules its token out (probability 0).  A row without any other logit, or with
  * a NaN or +inf, has no distribution: its outputs are NaN (NaN logits sort before all others).
- * Sums in fp32 over at most a few thousand terms each, joined in a fixed order, final
- * logarithms in fp64: results do not vary from run to run.  1 <= vocab <= ld < 2^31,
- * 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP, vocab).  Any alignment of the element type.
+ * fp32 sums of a few logits each, joined in fp64 in a fixed order: results do not vary from run to
+ * run.  1 <= vocab < 2^31 - 16, vocab <= ld < 2^31, 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP,
+ * vocab).  Any alignment of the element type.
  * Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
 zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int64_t rows, int64_t vocab,
                       int64_t ld, const int32_t *targets, float *logprob, float *entropy, int32_t top,

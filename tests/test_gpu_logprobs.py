@@ -301,6 +301,7 @@ def test_logprobs_refusals(zo, ctx):
         assert e.value.status == zo.ZO_ERR_INVALID
 
     refused(x=0)
+    refused(vocab=2 ** 31 - 16, ld=2 ** 31 - 1)
     refused(t=None)
     refused(dtype=5)
     refused(rows=0)

@@ -207,3 +207,64 @@ def test_captured_passes_of_two_contexts_side_by_side(zo):
     del graphs, g
     for c in ctxs:
         c.close()
+
+
+def test_calls_in_a_row_see_what_the_ones_before_wrote(zo, stream):
+    """Kernels may start before their predecessors have ended, and wait for them: long calls one right
+    behind another give what they give with a synchronisation between."""
+    ctx = zo.zo_create(torch.zeros(64, dtype=torch.bfloat16, device="cuda"), stream=stream)
+    n, lens = 6000, [2500, 30, 1470, 2000]
+    ld = (H + 2 * HK) * E
+    g = torch.Generator(device="cuda").manual_seed(5)
+    head = (torch.randn(20000, H * E, generator=g, device="cuda") * 0.1).to(torch.bfloat16)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    space = torch.empty(zo.zo_head_logprobs_workspace(n, 20000), dtype=torch.uint8, device="cuda")
+    logits = torch.empty(n, 3000, device="cuda")
+
+    def run(x, t, wait):
+        qkv, att = torch.zeros(n, ld, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, H * E, dtype=torch.bfloat16,
+                                                                                      device="cuda")
+        out = [torch.zeros(n, device="cuda") for _ in range(3)]
+        steps = [lambda: zo.zo_rope(ctx, x, qkv, None, ROPE, n, ld, ld, ld // E, E),
+                 lambda: zo.zo_attention_packed(ctx, qkv, qkv[:, H * E:], qkv[:, (H + HK) * E:], att, cu, len(lens), n, ld,
+                                                ld, ld, H * E, H, HK, E, E ** -0.5),
+                 lambda: zo.zo_head_logprobs(ctx, att, head, n, 20000, H * E, H * E, H * E, t, out[0], out[1], space),
+                 lambda: zo.zo_rope(ctx, att, att, None, ROPE, n, H * E, H * E, H, E),
+                 lambda: logits.zero_(),
+                 lambda: zo.zo_gemm_bf16(ctx, att, head, None, logits, n, 3000, H * E, 3000, zo.ZO_EPI_RESID_F32),
+                 lambda: zo.zo_logprobs(ctx, logits, n, 3000, 3000, None, None, out[2])]
+        for s in steps:
+            s()
+            if wait:
+                stream.synchronize()
+        return [qkv, att] + out
+
+    for _ in range(4):
+        x = torch.randn(n, ld, generator=g, device="cuda").to(torch.bfloat16)
+        t = torch.randint(0, 20000, (n,), generator=g, device="cuda", dtype=torch.int32)
+        got, want = run(x, t, False), run(x, t, True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert zo.zo_sync(ctx) == 0
+    ctx.close()
+
+
+def test_a_loss_pass_behind_an_operator_reads_what_it_wrote(zo, stream):
+    """The quadratic's pass streams theta and D as soon as it may start."""
+    rows, heads, e = 8192, 16, 64
+    m = rows * heads * e
+    theta = torch.randn(m, device="cuda")
+    ctx = zo.zo_create(theta, stream=stream)
+    x = torch.randn(rows, heads * e, device="cuda")
+    d = torch.zeros(m, device="cuda")
+    losses = torch.zeros(2, dtype=torch.float64, device="cuda")
+    for i in range(3):
+        for k, wait in enumerate((True, False)):
+            d.zero_()
+            stream.synchronize()
+            zo.zo_rope(ctx, x, d, None, dict(theta=1.0e4, rot_dim=e, magnitude=1.0 + i), rows, heads * e, heads * e, heads, e)
+            if wait:
+                stream.synchronize()
+            zo.zo_quad_loss(ctx, d, losses[k:])
+        assert zo.zo_sync(ctx) == 0
+        assert losses[0] != 0 and losses[0] == losses[1]
+    ctx.close()

@@ -277,6 +277,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;  // scores of stream i at column 128 i, output at 256 + HD i
+  tc::pdl_wait();  // the kernels ahead in the stream have ended
 
   auto give_up = [&]() {
     atomicOr(a.err, ZO_FLAG_TIMEOUT);

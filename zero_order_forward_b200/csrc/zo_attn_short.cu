@@ -52,7 +52,6 @@ attn_short_kernel(const __grid_constant__ PackedArgs a) {
   constexpr int kGroups = kShortSeq / 16;    // of 16 keys or rows
   extern __shared__ __align__(128) uint8_t smem[];
   tc::pdl_wait();
-  tc::pdl_launch_dependents();
   const int h = blockIdx.x, i = (int)(blockIdx.z * gridDim.y + blockIdx.y);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Seq seq = load_seq(a, i);

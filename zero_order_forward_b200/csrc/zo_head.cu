@@ -238,7 +238,7 @@ head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
           ++issued;
         }
       }
-      tc::pdl_launch_dependents();
+      tc::pdl_launch_dependents();  // (the joining kernel, which waits for this one's end at its start)
     } else if (warp == 1) {  // MMAs: the warp in step, one lane issues
       const uint32_t a0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sA), 0));
       const uint32_t b0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sB), 0));
@@ -417,7 +417,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           ++issued;
         }
       }
-      tc::pdl_launch_dependents();
+      tc::pdl_launch_dependents();  // (the joining kernel, which waits for this one's end at its start)
     } else if (warp == 1 && leader) {  // MMAs: the warp in step, one lane issues
       const uint32_t a0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sA), 0));
       const uint32_t b0 = tc::desc_k128_lo(__shfl_sync(0xFFFFFFFFu, tc::smem_addr(sB), 0));
@@ -518,7 +518,6 @@ __global__ void __launch_bounds__(256)
 head_join_kernel(HeadArgs a, float *logprob, float *entropy) {
   constexpr int N = (kSmCount + 31) / 32;  // triples of a lane (148 at most in all)
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  tc::pdl_launch_dependents();
   tc::pdl_wait();
   if (row >= a.rows) return;
   const float4 *part = a.part + (int64_t)row * a.splits;

@@ -241,7 +241,9 @@ zo_status step_device(zo_ctx *ctx, const double *loss_plus, const double *loss_m
                       const double *loss0, float lr, float eps, float damping);
 
 // Launch that may start before the kernel ahead of it in the stream has ended (its blocks wait
-// for that end themselves: tc::pdl_wait, before they touch anything but their own memory).
+// for that end themselves: tc::pdl_wait, before they touch anything but their own memory).  A kernel
+// that writes what a caller may hand on does not let its successor start early (only head_kernel does,
+// for the kernel that joins its partial results): the loss passes read theta and D before they wait.
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A &&...args) {
   cudaLaunchConfig_t cfg{};

@@ -318,7 +318,6 @@ logprobs_kernel(const LogprobArgs a) {
   const RowView<T> row(static_cast<const T *>(a.logits) + r * a.ld, a.vocab);
   const int j_first = (int)((int64_t)row.vectors * part / a.splits);
   const int j_end = (int)((int64_t)row.vectors * (part + 1) / a.splits);
-  tc::pdl_launch_dependents();
   if (tid == 0) sh.n_hot = sh.n_cand = 0;
   if (a.splits > 1) tc::cluster_arrive();  // block 0 has to run before its memory is written
   tc::pdl_wait();
@@ -587,8 +586,8 @@ extern "C" zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int
   if (!logits || (logprob && !targets)) return fail(ctx, ZO_ERR_INVALID, "null logprobs argument");
   if (dtype != ZO_F32 && dtype != ZO_BF16)
     return fail(ctx, ZO_ERR_INVALID, "logprobs: dtype must be fp32 or bf16");
-  if (rows < 1 || rows > INT32_MAX || vocab < 1 || ld < vocab || ld > INT32_MAX)
-    return fail(ctx, ZO_ERR_INVALID, "logprobs: need 1 <= rows < 2^31, 1 <= vocab <= ld < 2^31");
+  if (rows < 1 || rows > INT32_MAX || vocab < 1 || vocab > INT32_MAX - 16 || ld < vocab || ld > INT32_MAX)
+    return fail(ctx, ZO_ERR_INVALID, "logprobs: need 1 <= rows < 2^31, 1 <= vocab < 2^31 - 16, vocab <= ld < 2^31");
   if (top < 0 || top > ZO_MAX_TOP || top > vocab)
     return fail(ctx, ZO_ERR_INVALID, "logprobs: top outside [0, min(%d, vocab)]", ZO_MAX_TOP);
   if (!logprob && !entropy && (top == 0 || (!top_ids && !top_logprobs)))

@@ -89,7 +89,6 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   using Raw = typename P::Raw;
   constexpr bool kOne = IL && VEC > 1;           // a pair's features lie in one access
   constexpr int kPairs = kOne ? VEC / 2 : VEC;  // of a unit
-  tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int group = threadIdx.x / a.units, unit = threadIdx.x - group * a.units;
   const int groups = kRopeThreads / a.units;
