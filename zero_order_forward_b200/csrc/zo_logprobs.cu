@@ -307,6 +307,7 @@ template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS * rows_of_block(THREADS), 1024 / (THREADS * rows_of_block(THREADS)))
 logprobs_kernel(const LogprobArgs a) {
   constexpr int V = Row<T>::kVec, WARPS = THREADS / 32, U = 4;
+  constexpr int kMany = THREADS == 32 ? 26 : kManyHot;  // (nearly all lanes of a warp)
   using Sh = Shared<THREADS>;
   __shared__ Sh shared[rows_of_block(THREADS)];
   Sh &sh = shared[threadIdx.y];
@@ -402,7 +403,7 @@ logprobs_kernel(const LogprobArgs a) {
       }
     }
     uint64_t bound = (uint64_t)prefix << 48;
-    if (reach > kManyHot) {  // many alike: the exact key
+    if (reach > kMany) {  // many alike: the exact key
       k = block_merge<WARPS>(warp_sort(mine), sh.list);
       if (warp == 0 && lane == a.top - 1) sh.bound = k;
       row_sync<THREADS>();
@@ -422,7 +423,7 @@ logprobs_kernel(const LogprobArgs a) {
         }
       }
     };
-    if (reach > kManyHot) {
+    if (reach > kMany) {
       if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)tid;
       row_sync<THREADS>();
       for (int i = warp; i < sh.n_hot; i += WARPS)
