@@ -164,6 +164,17 @@ def test_ties_masks_and_bad_rows_where_a_block_has_a_row_of_its_own(zo, ctx, dty
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(2, 60000), (200, 20000), (900, 9000), (4000, 3000)])
+def test_sorted_rows(zo, ctx, dtype, rows, vocab):
+    """Rising and falling logits: far more than the alternatives lie within 1 % of the largest."""
+    up = torch.arange(vocab, device="cuda").float() / 64
+    x = torch.stack([up if i % 2 else 1000.0 - up for i in range(rows)]).to(TYPES[dtype])
+    t = torch.arange(rows, dtype=torch.int32, device="cuda") % vocab
+    for top in (1, 32):
+        check(x, t, call(zo, ctx, x, t, top), top)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab", [(1, 4099), (3, 9000), (40, 8300), (148, 5000), (149, 5000)])
 @pytest.mark.parametrize("shift", [0, 3])
 def test_rows_split_over_blocks(zo, ctx, dtype, rows, vocab, shift):

@@ -402,45 +402,55 @@ logprobs_kernel(const LogprobArgs a) {
         reach = n;
       }
     }
-    uint64_t bound = (uint64_t)prefix << 48;
-    if (reach > kMany) {  // many alike: the exact key
-      k = block_merge<WARPS>(warp_sort(mine), sh.list);
-      if (warp == 0 && lane == a.top - 1) sh.bound = k;
-      row_sync<THREADS>();
-      bound = sh.bound;  // 0: fewer threads than that have any logit
-    }
-    // vector jj again: its logits that reach the bound
-    auto gather = [&](int jj) {
-      float f[V];
-      Row<T>::open(row.read(jj), f);
+    // The prefix alone is the bound, unless many threads or too many logits reach it: then the exact key.
+    bool exact = reach > kMany;
+#pragma unroll 1
+    while (true) {
+      uint64_t bound = (uint64_t)prefix << 48;
+      if (exact) {
+        k = block_merge<WARPS>(warp_sort(mine), sh.list);
+        if (warp == 0 && lane == a.top - 1) sh.bound = k;
+        row_sync<THREADS>();
+        bound = sh.bound;  // 0: fewer threads than that have any logit
+      }
+      // vector jj again: its logits that reach the bound
+      auto gather = [&](int jj) {
+        float f[V];
+        Row<T>::open(row.read(jj), f);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t o = order_of(f[e]);
-        const int index = row.first(jj) + e;
-        if (key_of(o, (uint32_t)jj) >= bound && index >= 0 && index < a.vocab) {
-          const int at = atomicAdd(&sh.n_cand, 1);
-          if (at < Sh::kCandidates) sh.cand[at] = key_of(o, (uint32_t)index);
+        for (int e = 0; e < V; ++e) {
+          const uint32_t o = order_of(f[e]);
+          const int index = row.first(jj) + e;
+          if (key_of(o, (uint32_t)jj) >= bound && index >= 0 && index < a.vocab) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < Sh::kCandidates) sh.cand[at] = key_of(o, (uint32_t)index);
+          }
+        }
+      };
+      if (exact) {
+        if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)tid;
+        row_sync<THREADS>();
+        for (int i = warp; i < sh.n_hot; i += WARPS)
+          for (int jj = j_first + sh.hot[i] + lane * THREADS; jj < j_end; jj += 32 * THREADS) gather(jj);
+      } else {
+        if (mine != 0 && mine >= bound)
+          for (int g = 0; g < group; ++g)
+            if (sh.group_top[g][tid] >= prefix) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)(tid + THREADS * g);
+        row_sync<THREADS>();
+        const int per = U * group_rounds;  // vectors of a group
+        for (int i = tid; i < sh.n_hot * per; i += THREADS) {
+          const int h = sh.hot[i / per];
+          const int jj = j_first + h % THREADS + (h / THREADS * per + i % per) * THREADS;
+          if (jj < j_end) gather(jj);
         }
       }
-    };
-    if (reach > kMany) {
-      if (mine != 0 && mine >= bound) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)tid;
       row_sync<THREADS>();
-      for (int i = warp; i < sh.n_hot; i += WARPS)
-        for (int jj = j_first + sh.hot[i] + lane * THREADS; jj < j_end; jj += 32 * THREADS) gather(jj);
-    } else {
-      if (mine != 0 && mine >= bound)
-        for (int g = 0; g < group; ++g)
-          if (sh.group_top[g][tid] >= prefix) sh.hot[atomicAdd(&sh.n_hot, 1)] = (uint16_t)(tid + THREADS * g);
+      if (exact || sh.n_cand <= Sh::kCandidates) break;
       row_sync<THREADS>();
-      const int per = U * group_rounds;  // vectors of a group
-      for (int i = tid; i < sh.n_hot * per; i += THREADS) {
-        const int h = sh.hot[i / per];
-        const int jj = j_first + h % THREADS + (h / THREADS * per + i % per) * THREADS;
-        if (jj < j_end) gather(jj);
-      }
+      if (tid == 0) sh.n_hot = sh.n_cand = 0;
+      row_sync<THREADS>();
+      exact = true;
     }
-    row_sync<THREADS>();
     const int n_list = sh.n_cand;
     if (n_list > 32) {
       if (n_list <= Sh::kCandidates) {
