@@ -488,10 +488,9 @@ class zo_rope_cfg(ctypes.Structure):
     @classmethod
     def from_dict(cls, c):
         scaling = c.get("scaling", "none")
-        return cls(float(c["theta"]), int(c["rot_dim"]), int(bool(c.get("interleaved", False))),
-                   ROPE_SCALINGS.get(scaling, scaling), float(c.get("factor", 1.0)),
-                   float(c.get("orig_len", 0.0)), float(c.get("band_low", 0.0)),
-                   float(c.get("band_high", 0.0)), float(c.get("magnitude", 1.0)))
+        return cls(c["theta"], int(c["rot_dim"]), bool(c.get("interleaved", False)),
+                   ROPE_SCALINGS.get(scaling, scaling), c.get("factor", 1.0), c.get("orig_len", 0.0),
+                   c.get("band_low", 0.0), c.get("band_high", 0.0), c.get("magnitude", 1.0))
 
 
 def _rope_cfg(cfg):

@@ -617,21 +617,21 @@ extern "C" zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void 
   const DeviceScope device(ctx);
   if (device.status != cudaSuccess)
     return fail(ctx, ZO_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(device.status));
-  CUtensorMap tmq, tmk, tmv;
-  if (!tile_map_bf16(&tmq, q, total_tokens, wq, ldq, kM) || !tile_map_bf16(&tmk, k, total_tokens, wk, ldk, kM) ||
-      !tile_map_bf16(&tmv, v, total_tokens, wk, ldv, kM))
-    return fail(ctx, ZO_ERR_CUDA, "attention_packed: cuTensorMapEncodeTiled failed");
   const int shared = n_heads / n_kv_heads;
   const Mode mode = shared % 2 == 0 ? kHeads : head_dim == 64 && shared == 1 && n_heads % 2 == 0 ? kPair64 : kRows;
   PackedArgs a{static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
-                     static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out), cu_seqlens, n_seqs,
-                     (int)total_tokens, n_heads, n_kv_heads, ldq, ldk, ldv, ldo,
-                     scale * 1.4426950408889634f, (int)mode, shared, 0, &ctx->dstate->flags};
+               static_cast<const uint16_t *>(v), static_cast<uint16_t *>(out), cu_seqlens, n_seqs,
+               (int)total_tokens, n_heads, n_kv_heads, ldq, ldk, ldv, ldo,
+               scale * 1.4426950408889634f, (int)mode, shared, 0, &ctx->dstate->flags};
   if (total_tokens / n_seqs <= kShortMean) {
     const zo_status st = launch_attn_short(ctx, a, head_dim);
     if (st != ZO_OK || total_tokens <= kShortSeq) return st;
     a.handled = kShortSeq;
   }
+  CUtensorMap tmq, tmk, tmv;
+  if (!tile_map_bf16(&tmq, q, total_tokens, wq, ldq, kM) || !tile_map_bf16(&tmk, k, total_tokens, wk, ldk, kM) ||
+      !tile_map_bf16(&tmv, v, total_tokens, wk, ldv, kM))
+    return fail(ctx, ZO_ERR_CUDA, "attention_packed: cuTensorMapEncodeTiled failed");
   if (head_dim == 128) return launch<128, false>(ctx, tmq, tmk, tmv, a);
   return mode == kPair64 ? launch<64, true>(ctx, tmq, tmk, tmv, a) : launch<64, false>(ctx, tmq, tmk, tmv, a);
 }
