@@ -46,8 +46,8 @@ constexpr int kItems = 2;              // items on hand
 
 // Sequences of at most kShortSeq tokens go to a kernel of their own where the mean length (the buffer's
 // over their number; lengths are known on the device only) lets there be many of them.  16 heads of
-// 128: 64 sequences of 16 tokens take 7.8 us instead of 16.4, 64 of 32 9.7 instead of 17; 64 of 64, of
-// which it finds none, 20.4 instead of 18.7, and sequences of some thousand tokens as much more.
+// 128: 64 sequences of 16 tokens take 7.8 us instead of 16.4, 64 of 32 9.7 instead of 16.4; 64 of 64, of
+// which it finds none, 20.6 instead of 19.2, and sequences of some thousand tokens as much more.
 constexpr int kShortMean = 256;
 
 enum Mode { kHeads, kPair64, kRows };
