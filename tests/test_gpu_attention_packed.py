@@ -366,3 +366,62 @@ def test_packed_attention_refusals(zo, ctx):
     refused(status=zo.ZO_ERR_UNSUPPORTED, hd=96)
     torch.cuda.synchronize()
     assert torch.all(out == 2.0)
+
+
+def by_definition(q, k, v, lens, H, Hk, hd, scale):
+    """(fp64 output with infinities and NaN where the sum over a row's own keys has them, tolerance of
+    the finite ones).  Weights are taken as positive wherever the score is not -inf or NaN."""
+    fill = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    ref, tol = reference(q, k, fill, lens, H, Hk, hd, scale)
+    at = 0
+    for n in lens:
+        V = v[at: at + n].reshape(n, Hk, hd).repeat_interleave(H // Hk, 1).reshape(n, H * hd)
+        up, down = (V == math.inf).cumsum(0) > 0, (V == -math.inf).cumsum(0) > 0
+        nan = (torch.isnan(V).cumsum(0) > 0) | (up & down)
+        o = ref[at: at + n]
+        o[up] = math.inf
+        o[down] = -math.inf
+        o[nan] = math.nan
+        at += n
+    return ref, tol
+
+
+def same_or_close(out, ref, tol):
+    """Where the reference is finite, within tol; elsewhere the same infinity, or NaN."""
+    out = out.double()
+    close = torch.isfinite(ref) & ((out - ref).abs() <= tol)
+    return close | (out == ref) | (torch.isnan(out) & torch.isnan(ref))
+
+
+# sequences, and (row, own column's value) before (row, later value) of one sequence
+OWN_AND_LATER = [([260], 0, 130, 170),           # inside the second tile's diagonal
+                 ([40, 500, 300], 1, 3, 100),    # the first tile, between other sequences
+                 ([700], 0, 10, 650),            # own value tiles ahead of the diagonal one
+                 ([30, 9], 0, 3, 9),             # short sequences: one group of 16 keys
+                 ([30, 9], 0, 3, 25)]            # the second group
+
+
+@pytest.mark.parametrize("H,Hk,hd", [(4, 2, 128), (4, 2, 64), (2, 2, 64), (3, 3, 64), (1, 1, 128)])
+@pytest.mark.parametrize("lens,seq,own,late", OWN_AND_LATER)
+@pytest.mark.parametrize("first", [math.inf, -math.inf])
+@pytest.mark.parametrize("then", [math.nan, math.inf, -math.inf])
+def test_own_infinities_stand_beside_later_bad_values(zo, ctx, H, Hk, hd, lens, seq, own, late, first, then):
+    """A value column with an infinity of a row's own and a bad value of a later token: the infinity, up to
+    the later token.  Columns that hold nothing bad keep the bits that they have without it."""
+    qkv = make(lens, H, Hk, hd)
+    clean = torch.zeros(sum(lens), H * hd, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, clean, offsets(lens), H, Hk, hd)
+    q, k, v = split(qkv, H, Hk, hd)
+    row0 = sum(lens[:seq])
+    v[row0 + own, 5] = first
+    v[row0 + late, 5] = then
+    v[row0 + late, hd - 3] = then     # a column with nothing bad before
+    v[row0 + own, 9] = first          # one with nothing bad behind
+    out = torch.zeros_like(clean)
+    call(zo, ctx, qkv, out, offsets(lens), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    ref, tol = by_definition(q, k, v, lens, H, Hk, hd, 1 / math.sqrt(hd))
+    ok = same_or_close(out, ref, tol)
+    assert ok.all(), (~ok).nonzero()[:8].tolist()
+    good = [c for c in range(H * hd) if c % hd not in (5, 9, hd - 3)]
+    assert torch.equal(out[:, good], clean[:, good])

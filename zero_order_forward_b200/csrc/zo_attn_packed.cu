@@ -23,8 +23,8 @@
 //     (or padding): their scores are masked, groups of 16 keys behind the sequence are not
 //     multiplied, and value rows behind it in its last group are cleared in shared memory;
 //   - within the diagonal tile a later token's value row is multiplied by probability 0, which is
-//     not 0 for an infinity or NaN: a row whose output is not finite is looked at again
-//     (repair_rows) and recomputed from its own keys alone where a later row is to blame.
+//     not 0 for an infinity or NaN: a row whose output is not finite is looked at again (repair_rows),
+//     and its columns that a later value reached are computed from its own keys alone.
 #include <cmath>
 
 #include "zo_attn_packed.cuh"

@@ -33,10 +33,12 @@ __device__ __forceinline__ Seq load_seq(const PackedArgs &a, int i) {
 
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) != 0x7F80u; }
 
-// Rows first + (bits of `rows`) of the tile came out infinite or NaN.  That is right if a value
-// row that they attend to says so; it is wrong where only a later row of the tile's last keys
-// (up to key_end) does.  One warp: a row with a non-finite later value row, and with a non-finite
-// output that no own key's value explains, is computed again from keys 0 .. r alone, in fp32.
+// Rows first + (bits of `rows`) of the tile came out infinite or NaN somewhere.  That is right if a
+// value row that they attend to says so, but in the tile's last keys (up to key_end) a later row's
+// infinity or NaN reaches them as well, as 0 * infinity = NaN.  So a column with such an output and a
+// non-finite later value is computed again from the row's own keys, in fp32, whatever they hold; the
+// row's other columns stay.  One warp: key by key from the row's own backwards, 32 at a time, until
+// each such column is NaN for good.
 template <int HD>
 __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len, int first, uint32_t rows,
                                          int h, int kvh, int key_end) {
@@ -46,29 +48,33 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len,
   const uint16_t *V = a.v + (int64_t)row0 * a.ldv + kvh * HD + C * lane;
   for (; rows; rows &= rows - 1) {
     const int r = first + __ffs(rows) - 1;
-    bool later = false;
+    uint16_t *orow = a.out + (int64_t)(row0 + r) * a.ldo + h * HD + C * lane;
+    uint32_t open = 0;  // this lane's columns to compute again
     for (int j = r + 1; j < min(key_end, len); ++j)
 #pragma unroll
-      for (int c = 0; c < C; ++c) later |= !finite_bf16(V[(int64_t)j * a.ldv + c]);
-    if (!__any_sync(0xFFFFFFFFu, later)) continue;
-    uint16_t *orow = a.out + (int64_t)(row0 + r) * a.ldo + h * HD + C * lane;
-    uint32_t open = 0;  // this lane's non-finite outputs not explained yet
+      for (int c = 0; c < C; ++c) open |= finite_bf16(V[(int64_t)j * a.ldv + c]) ? 0u : 1u << c;
 #pragma unroll
-    for (int c = 0; c < C; ++c) open |= finite_bf16(orow[c]) ? 0u : 1u << c;
-    for (int j = 0; j <= r && __any_sync(0xFFFFFFFFu, open); ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (!finite_bf16(V[(int64_t)j * a.ldv + c])) open &= ~(1u << c);
+    for (int c = 0; c < C; ++c)
+      if (finite_bf16(orow[c])) open &= ~(1u << c);
     if (!__any_sync(0xFFFFFFFFu, open)) continue;
     const uint16_t *q = a.q + (int64_t)(row0 + r) * a.ldq + h * HD;
     float m = -INFINITY, l = 0.f, acc[C] = {};
-    for (int j0 = 0; j0 <= r; j0 += 32) {
-      const int j = j0 + lane;
+    for (int j0 = r; j0 >= 0; j0 -= 32) {  // keys j0, j0 - 1, ..
+      const int j = j0 - lane;
       float s = -INFINITY;
-      if (j <= r) {
+      if (j >= 0) {
         s = 0.f;
-        for (int e = 0; e < HD; ++e)
-          s = fmaf(bf16_bits_to_f32(q[e]), bf16_bits_to_f32(K[(int64_t)j * a.ldk + e]), s);
+#pragma unroll 1
+        for (int e = 0; e < HD; e += 8) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(q + e);
+          const uint4 y = *reinterpret_cast<const uint4 *>(K + (int64_t)j * a.ldk + e);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            s = fmaf(__uint_as_float(u[t] << 16), __uint_as_float(w[t] << 16), s);
+            s = fmaf(__uint_as_float(u[t] & 0xFFFF0000u), __uint_as_float(w[t] & 0xFFFF0000u), s);
+          }
+        }
         s *= a.scale_log2;
       }
       float mx = s;
@@ -76,7 +82,7 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len,
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
       mx = fmaxf(mx, m);
       const float ref = mx == -INFINITY ? 0.f : mx;
-      const float f = tc::ex2(m - ref), p = j <= r ? tc::ex2(s - ref) : 0.f;
+      const float f = tc::ex2(m - ref), p = j >= 0 ? tc::ex2(s - ref) : 0.f;
       float sum = p;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -84,15 +90,21 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len,
       m = mx;
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[c] *= f;
-      for (int t = 0; t < 32 && j0 + t <= r; ++t) {
+#pragma unroll 4
+      for (int t = 0; t < min(32, j0 + 1); ++t) {
         const float pt = __shfl_sync(0xFFFFFFFFu, p, t);
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          acc[c] = fmaf(pt, bf16_bits_to_f32(V[(int64_t)(j0 + t) * a.ldv + c]), acc[c]);
+          acc[c] = fmaf(pt, bf16_bits_to_f32(V[(int64_t)(j0 - t) * a.ldv + c]), acc[c]);
       }
+      bool more = false;  // (a NaN stays one)
+#pragma unroll
+      for (int c = 0; c < C; ++c) more |= (open >> c & 1u) && acc[c] == acc[c];
+      if (!__any_sync(0xFFFFFFFFu, more)) break;
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) orow[c] = f32_to_bf16_bits(acc[c] / l);
+    for (int c = 0; c < C; ++c)
+      if (open >> c & 1u) orow[c] = f32_to_bf16_bits(acc[c] / l);
   }
 }
 
