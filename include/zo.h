@@ -672,7 +672,7 @@ zo_status zo_rope(zo_ctx *ctx, const void *x, void *out, int dtype, const int32_
  *               may be empty.  Rows of out outside every sequence are not written.
  *   scale       finite and > 0 (1/sqrt(head_dim) for the decoders here).
  * fp32 scores and sums, probabilities rounded to bf16 for the second product, one bf16 rounding
- * of the output.  A row depends on its sequence's rows up to itself only, whatever the other
+ * of the output.  A score of -inf has weight 0; a row of no other is NaN.  A row depends on its sequence's rows up to itself only, whatever the other
  * rows hold (infinities and NaN too); its last bits may differ between calls of other total_tokens
  * or n_seqs, which choose among kernels, and in a value column where a later token's is infinite or NaN.
  * The offsets are read on the device: a decreasing or

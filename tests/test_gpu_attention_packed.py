@@ -425,3 +425,41 @@ def test_own_infinities_stand_beside_later_bad_values(zo, ctx, H, Hk, hd, lens, 
     assert ok.all(), (~ok).nonzero()[:8].tolist()
     good = [c for c in range(H * hd) if c % hd not in (5, 9, hd - 3)]
     assert torch.equal(out[:, good], clean[:, good])
+
+
+@pytest.mark.parametrize("H,Hk,hd", [(4, 2, 128), (2, 2, 64), (3, 3, 64), (1, 1, 128)])
+@pytest.mark.parametrize("lens", [[300, 150], [12, 30, 1]])
+def test_rows_whose_every_score_is_ruled_out_are_nan(zo, ctx, H, Hk, hd, lens):
+    """Keys that give a score of -inf have no weight; a row with no other key has no softmax."""
+    qkv = make(lens, H, Hk, hd)
+    q, k, v = split(qkv, H, Hk, hd)
+    q.view(-1, H, hd)[:, :, 0] = 1.0
+    dead = {0: lens[0] // 2, 1: 2}                     # leading keys of the first two sequences
+    at = np.cumsum([0] + lens)
+    for i, n in dead.items():
+        k.view(-1, Hk, hd)[at[i]: at[i] + n, :, 0] = -math.inf
+    k.view(-1, Hk, hd)[at[1] + 5, :, 0] = -math.inf    # one key among others
+    out = torch.zeros(sum(lens), H * hd, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets(lens), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    none = torch.zeros(sum(lens), dtype=torch.bool, device="cuda")
+    for i, n in dead.items():
+        none[at[i]: at[i] + n] = True
+    assert torch.isnan(out[none]).all()
+    # the others as if those keys were not there
+    alive = torch.isfinite(k[:, 0]).tolist()
+    for i, n in enumerate(lens):
+        for r in range(n):
+            if none[at[i] + r] or (r % 7 and r < n - 3):
+                continue
+            keep = [j for j in range(at[i], at[i] + r + 1) if alive[j]]
+            for h in range(H):
+                g = h // (H // Hk)
+                K, V = k[keep, g * hd: (g + 1) * hd].double(), v[keep, g * hd: (g + 1) * hd].double()
+                Q = q[at[i] + r, h * hd: (h + 1) * hd].double()
+                s = K @ Q / math.sqrt(hd)
+                w = torch.softmax(s, 0)
+                ref, A = w @ V, w @ V.abs()
+                e = 2 * hd * 2.0 ** -23 * (K.abs() @ Q.abs()).max() / math.sqrt(hd) + 2.0 ** -23 * s.abs().max()
+                tol = 1.02 * (A * (2.0 ** -8 + 2.0 ** -20 + 2 * e) + 2.0 ** -8 * ref.abs())
+                assert torch.all((out[at[i] + r, h * hd: (h + 1) * hd].double() - ref).abs() <= tol)

@@ -526,7 +526,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       if (!ok) break;
       if (!tc::warp_wait_fast(&pv_done[i], (done - 1u) & 1u, abort_flag)) { ok = false; break; }
       tc::tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = 1.f / l;  // (l = 0: every score of the row is -inf, and 0 infinity = NaN)
       const int r_quad = r - lane % 4;
       uint16_t *orow = a.out + (int64_t)(w.row0 + r_quad) * a.ldo + (int64_t)head * HD + 8 * (lane % 4);
       uint32_t worst = 0;  // two bf16, NaN if any output of the row is not finite

@@ -169,7 +169,7 @@ attn_short_kernel(const __grid_constant__ PackedArgs a) {
   for (int x = 0; x < 2; ++x) {
     l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 1);
     l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 2);
-    inv[x] = l[x] > 0.f ? 1.f / l[x] : 0.f;
+    inv[x] = 1.f / l[x];  // (l = 0: every score of the row is -inf, and 0 infinity = NaN)
   }
   uint16_t *out = a.out + (int64_t)(seq.row0 + r) * a.ldo + h * HD + 8 * (lane % 4);
   uint32_t worst[2] = {0, 0};  // bf16 pairs, not 0 (NaN) if any output of the row is not finite
