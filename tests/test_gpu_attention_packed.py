@@ -463,3 +463,48 @@ def test_rows_whose_every_score_is_ruled_out_are_nan(zo, ctx, H, Hk, hd, lens):
                 e = 2 * hd * 2.0 ** -23 * (K.abs() @ Q.abs()).max() / math.sqrt(hd) + 2.0 ** -23 * s.abs().max()
                 tol = 1.02 * (A * (2.0 ** -8 + 2.0 ** -20 + 2 * e) + 2.0 ** -8 * ref.abs())
                 assert torch.all((out[at[i] + r, h * hd: (h + 1) * hd].double() - ref).abs() <= tol)
+
+
+def scattered(n_seqs, lens, seed=0):
+    """n_seqs lengths, all 0 but `lens`, which lie at random places, the last of all among them."""
+    r = np.random.default_rng(seed)
+    at = np.sort(r.choice(n_seqs - 1, len(lens) - 1, replace=False)).tolist() + [n_seqs - 1]
+    out = np.zeros(n_seqs, dtype=np.int64)
+    out[at] = lens
+    return out
+
+
+@pytest.mark.parametrize("H,Hk,hd", [(2, 1, 128), (2, 2, 64), (1, 1, 64)])
+@pytest.mark.parametrize("n_seqs,lens", [
+    (3000, [2000]), (3000, [1, 700, 33, 2000, 129]), (300000, [5000, 3, 1100, 64, 1100, 400]),
+    (40000, [40 * k + 33 for k in range(60)]),            # more long ones than lanes, many distinct lengths
+    ((1 << 20) + 77, [1300, 40, 900, 300, 2000, 128, 129, 700]),  # items of no tiles between the others
+    ((1 << 20) + 77, [150 * k + 40 for k in range(40)])])
+def test_few_long_sequences_among_many_empty_ones(zo, ctx, H, Hk, hd, n_seqs, lens):
+    qkv = make(lens, H, Hk, hd)
+    out = torch.zeros(sum(lens), H * hd, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets(scattered(n_seqs, lens)), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    check(zo, ctx, qkv, out, lens, H, Hk, hd)
+
+
+def test_a_long_sequence_among_many_empty_ones_costs_few_scans(zo):
+    """16384 tokens among 131072 sequences: 128 numbers of tiles, of which two occur.  A scan for every one
+    of them takes more than 100 ms, one for every one that occurs a few."""
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        c = zo.zo_create(torch.zeros(64, device="cuda"), stream=s)
+        qkv = make([16384], 2, 1, 64)
+        out = torch.zeros(16384, 128, dtype=torch.bfloat16, device="cuda")
+        cu = offsets(scattered(131072, [16384]))
+        times = []
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record(s)
+            call(zo, c, qkv, out, cu, 2, 1, 64)
+            b.record(s)
+            s.synchronize()
+            times.append(a.elapsed_time(b))
+    assert zo.zo_sync(c) == 0
+    assert min(times) < 30.0, times
+    c.close()

@@ -147,3 +147,49 @@ def test_long_items_are_spread():
 def test_bad_offsets_have_no_items(cu):
     good = {i for i, (s, e) in enumerate(zip(cu[:-1], cu[1:])) if 0 <= s <= e <= 32}
     assert {s for _, s, _, _ in _items(cu, 32, 128, 1, 4)} == {i for i in good if cu[i + 1] > cu[i]}
+
+
+def _items_by_distinct_lengths(cu, total, rows, group, grid):
+    """_items with a scan of the offsets only where the set of long enough sequences changes: it is the
+    same from a number of tiles down to the next one that occurs.  Yields (scans so far, item)."""
+    tiles = []
+    for s, e in zip(cu[:-1], cu[1:]):
+        bad = s < 0 or e < s or e > total
+        tiles.append(0 if bad else (e - s + rows - 1) // rows)
+    items = sum(tiles) * group
+
+    def scan(level):
+        return [i for i, t in enumerate(tiles) if t > level], max((t for t in tiles if t <= level), default=0)
+
+    for cta in range(grid):
+        level = max(tiles) - 1
+        base = n = 0
+        scans = 1
+        held, below = scan(level) if level >= 0 else ([], 0)
+        while True:
+            back = n % 2 == 1 or (n > 0 and (n + 1) * grid >= items)
+            slot = n * grid + (grid - 1 - cta if back else cta)
+            n += 1
+            while level >= 0 and slot >= base + len(held) * group:
+                base += len(held) * group
+                level -= 1
+                if 0 <= level < below:
+                    held, below = scan(level)
+                    scans += 1
+            if level < 0:
+                break
+            index = slot - base
+            yield scans, (cta, held[index // group], level, index % group)
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 5], [128, 129, 127], [0, 1000, 0, 1, 2], [5000, 0, 0, 0, 1],
+                                  [2000, 3, 700, 700, 128, 256, 257], [300 * k for k in range(9)]])
+@pytest.mark.parametrize("rows,group", [(128, 3), (256, 1)])
+def test_scans_of_distinct_lengths_find_the_same_items(lens, rows, group):
+    cu = [0] + np.cumsum(lens).tolist()
+    total = max(1, cu[-1])
+    distinct = len({(n + rows - 1) // rows for n in lens if n})
+    for grid in (1, 7, 148):
+        got = list(_items_by_distinct_lengths(cu, total, rows, group, grid))
+        assert [i for _, i in got] == list(_items(cu, total, rows, group, grid))
+        assert all(s <= distinct for s, _ in got)

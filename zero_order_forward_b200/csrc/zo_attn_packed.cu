@@ -50,6 +50,10 @@ constexpr int kItems = 2;              // items on hand
 // which it finds none, 20.6 instead of 19.2, and sequences of some thousand tokens as much more.
 constexpr int kShortMean = 256;
 
+// From this many sequences on, up to 32 long ones among them are held in the lanes of the warp that
+// deals out the items, which is then spared a search for each.
+constexpr int kManySeqs = 1024;
+
 enum Mode { kHeads, kPair64, kRows };
 
 template <int HD, bool SPLIT>  // SPLIT: the streams have key/value heads of their own (kPair64)
@@ -70,7 +74,7 @@ struct PackedSmem {
 struct alignas(16) Item {
   int row0, len;  // the sequence's first row and length (0: no more items)
   int kvh;        // key/value head (of stream 0)
-  int most;       // key tiles of the longer stream
+  int most;       // key tiles of the longer stream (0: nothing to do)
   int q[2];       // first query row
   int head[2];    // query head
   int keys[2];    // keys of the stream's tile (0: no such stream)
@@ -98,13 +102,59 @@ __device__ __forceinline__ Item make_item(const PackedArgs &a, int row0, int len
   return it;
 }
 
+// Tiles of 2^shift rows of a sequence that are this kernel's.
+__device__ __forceinline__ int tiles_of(const PackedArgs &a, int shift, const Seq &s) {
+  return s.len <= a.handled ? 0 : (int)(((uint32_t)s.len + (1u << shift) - 1u) >> shift);
+}
+
+// What one warp finds in the sequences from the 33rd on.
+struct Scan {
+  int longer, below;  // sequences of more than `level` tiles; the most tiles of the others
+  int tiles;          // of all (each lane its own)
+  bool bad;
+};
+__device__ __forceinline__ Scan scan_rest(const PackedArgs &a, int shift, int level) {
+  const int lane = threadIdx.x & 31;
+  Scan f{0, 0, 0, false};
+#pragma unroll 1
+  for (int i0 = 32; i0 < a.n_seqs; i0 += 32) {
+    const Seq s = load_seq(a, i0 + lane);
+    const int t = tiles_of(a, shift, s);
+    f.longer += t > level ? 1 : 0;
+    f.below = max(f.below, t > level ? 0 : t);
+    f.tiles += t;
+    f.bad |= s.bad;
+  }
+  return f;
+}
+// The number of the lane-th of the `count` (at most 32) sequences of more than `level` tiles.
+__device__ __forceinline__ int hold(const PackedArgs &a, int shift, int level, int count) {
+  const int lane = threadIdx.x & 31;
+  int held = 0;
+#pragma unroll 1
+  for (int i0 = 0, got = 0; got < count && i0 < a.n_seqs; i0 += 32) {
+    uint32_t in = __ballot_sync(0xFFFFFFFFu, tiles_of(a, shift, load_seq(a, i0 + lane)) > level);
+#pragma unroll 1
+    for (; in; in &= in - 1, ++got)
+      if (lane == got) held = i0 + __ffs(in) - 1;
+  }
+  return held;
+}
+
 // The items of one CTA in their order (one warp).
+//
+// The offsets are scanned once for every distinct number of tiles that occurs (as many sequences have
+// more than t tiles for all t between two such numbers); where the offsets are many, up to 32 sequences
+// that are that long are held in the lanes.  One sequence of 16384 tokens among 131072 empty ones took
+// 137 ms with a scan for every number of tiles, 3.2 so.
 struct Schedule {
   const PackedArgs &a;
   int shift, group;        // log2 of a tile's rows; items of one tile (heads, or pairs of them)
   int lane;
   Seq first;               // this lane's of the first 32 sequences
-  int level, count;        // sequences with more than `level` tiles: `count`
+  int level, count;        // sequences with more than `level` tiles: `count`,
+  int below;               // the same ones as with more than `below`
+  int held;                // the lane-th of them, if there are few()
   int64_t base, total;     // items of the longer levels; of all
   int longest;             // tiles of the longest sequence
   int from, before;        // sequences [0, from) have `before` of the level's
@@ -114,55 +164,79 @@ struct Schedule {
     from = before = 0;
     group = a.mode == kRows ? a.H : a.H / 2;
     first = load_seq(a, lane);
-    int most = tiles_of(first), tiles = most;  // (fewer than 2^25 in all)
+    int tiles = tiles_of(first), most = tiles;  // (fewer than 2^25 in all)
     bool bad = first.bad;
-    for (int i0 = 32; i0 < a.n_seqs; i0 += 32) {
-      const Seq s = load_seq(a, i0 + lane);
-      most = max(most, tiles_of(s));
-      tiles += tiles_of(s);
-      bad |= s.bad;
+    if (a.n_seqs > 32) {
+      const Scan f = scan_rest(a, shift, INT32_MAX);
+      most = max(most, f.below);
+      tiles += f.tiles;
+      bad |= f.bad;
     }
     if (blockIdx.x == 0 && bad) atomicOr(a.err, ZO_FLAG_OFFSETS);
     total = (int64_t)__reduce_add_sync(0xFFFFFFFFu, tiles) * group;
     longest = __reduce_max_sync(0xFFFFFFFFu, most);
     level = longest - 1;
     base = 0;
-    count = level >= 0 ? sequences() : 0;
+    count = below = 0;
+    held = 0;
+    if (level >= 0) count_level();
   }
-  __device__ __forceinline__ int tiles_of(const Seq &s) const {
-    return s.len <= a.handled ? 0 : (int)(((uint32_t)s.len + (1u << shift) - 1u) >> shift);
+  __device__ __forceinline__ int tiles_of(const Seq &s) const { return zo::tiles_of(a, shift, s); }
+  __device__ __forceinline__ bool few() const { return a.n_seqs > kManySeqs && count <= 32; }
+  // One scan for the new `level` (two where the sequences are held).
+  __device__ __forceinline__ void count_level() {
+    const int t = tiles_of(first);
+    count = __popc(__ballot_sync(0xFFFFFFFFu, t > level));
+    below = __reduce_max_sync(0xFFFFFFFFu, t > level ? 0 : t);
+    if (a.n_seqs > 32) {
+      const Scan f = scan_rest(a, shift, level);
+      count += __reduce_add_sync(0xFFFFFFFFu, f.longer);
+      below = max(below, __reduce_max_sync(0xFFFFFFFFu, f.below));
+      if (few()) held = hold(a, shift, level, count);
+    }
   }
-  __device__ __forceinline__ bool has(int i0) const {
-    return tiles_of(i0 == 0 ? first : load_seq(a, i0 + lane)) > level;
+  // Slot of this CTA's round `n`: to and fro; the last round, which has items for some CTAs only, for
+  // those with the least so far.
+  __device__ __forceinline__ int64_t slot(int n) const {
+    const bool back = (n & 1) || (n > 0 && (int64_t)(n + 1) * gridDim.x >= total);
+    return (int64_t)n * gridDim.x + (back ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x);
   }
-  __device__ __forceinline__ int sequences() const {
-    int n = 0;
-    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, has(i0)));
-    return n;
-  }
-  // Item `slot`; slots must not decrease from call to call.
+  // Item `slot`; slots must not decrease from call to call.  After kPatience steps (of 32 sequences)
+  // of scans it returns an item of no tiles and goes on when called again, so that the warps that wait
+  // for items never do so for more than five scans: 2^19 steps of 0.26 us each at 2^24 sequences, 0.7 s
+  // in all, a third of their limit.
   __device__ __forceinline__ Item at(int64_t slot) {
+    constexpr int kPatience = 1 << 15;
+    Item it{};
+    int steps = 0;
     while (level >= 0 && slot >= base + (int64_t)count * group) {
       base += (int64_t)count * group;
       --level;
       from = before = 0;
-      if (level >= 0) count = sequences();
+      if (level >= 0 && level < below) {
+        count_level();
+        if ((steps += (a.n_seqs + 31) / 32) > kPatience) {
+          it.len = 1;
+          it.row0 = -1;
+          return it;
+        }
+      }
     }
-    Item it{};
     if (level < 0) return it;
     const int index = (int)(slot - base);
     const int nth = index / group;
+    if (few()) {
+      const Seq s = load_seq(a, __shfl_sync(0xFFFFFFFFu, held, nth));
+      return make_item(a, s.row0, s.len, level, index - nth * group);
+    }
     for (; from < a.n_seqs; from += 32) {
-      const uint32_t in = __ballot_sync(0xFFFFFFFFu, has(from));
+      const Seq s = from == 0 ? first : load_seq(a, from + lane);
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, tiles_of(s) > level);
       if (nth < before + __popc(in)) {
         const uint32_t lower = in & ((1u << lane) - 1u);
-        const int i = from + __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && before + __popc(lower) == nth)) - 1;
-        int row0 = __shfl_sync(0xFFFFFFFFu, first.row0, i & 31), len = __shfl_sync(0xFFFFFFFFu, first.len, i & 31);
-        if (from > 0) {
-          row0 = __ldg(a.cu + i);
-          len = __ldg(a.cu + i + 1) - row0;
-        }
-        it = make_item(a, row0, len, level, index - nth * group);
+        const int i = __ffs(__ballot_sync(0xFFFFFFFFu, (in >> lane & 1u) && before + __popc(lower) == nth)) - 1;
+        it = make_item(a, __shfl_sync(0xFFFFFFFFu, s.row0, i), __shfl_sync(0xFFFFFFFFu, s.len, i), level,
+                       index - nth * group);
         break;
       }
       before += __popc(in);
@@ -318,9 +392,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
           Item w;
           ok = next_item(n, w);
           if (!ok || w.len == 0) break;
-          ok = wait(q_empty, ((uint32_t)n & 1u) ^ 1u);
+          if (w.most == 0) continue;
+          ok = wait(q_empty, ((uint32_t)n_q & 1u) ^ 1u);
           if (!ok) break;
-          n_q = n + 1;
+          ++n_q;
           tc::mbar_arrive_expect_tx(q_full, (w.tiles[1] ? 2 : 1) * SM::kQTile);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -345,6 +420,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       uint32_t done[2] = {0, 0}, outs[2] = {0, 0};  // tiles and items of each stream so far
       tc::RingPos<NS> key[2], val;                  // of the next key tile for each stream; of the value tile
       val.next();
+      uint32_t n_q = 0;
       for (int n = 0; ok; ++n) {
         if (!tc::warp_wait_fast(&item_full[n % kItems], ring_parity(n, kItems), abort_flag)) { ok = false; break; }
         Item w = items[n % kItems];
@@ -359,6 +435,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
           w.tiles[i] = __shfl_sync(0xFFFFFFFFu, w.tiles[i], 0);
         }
         if (w.len == 0) break;
+        if (w.most == 0) continue;
         // K_j is there (it is for the second stream if the first has used it)
         auto wait_k = [&](int i, int j) -> bool {
           return (i == 1 && j < w.tiles[0]) || tc::warp_wait_fast(&full[key[i].slot], key[i].phase, abort_flag);
@@ -387,7 +464,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
           }
           __syncwarp();
         };
-        ok = tc::warp_wait_fast(q_full, (uint32_t)n & 1u, abort_flag) && wait_k(0, 0);
+        ok = tc::warp_wait_fast(q_full, n_q++ & 1u, abort_flag) && wait_k(0, 0);
         if (ok) {
           issue_s(0, 0);
           if (w.tiles[1]) issue_s(1, 0);
@@ -443,11 +520,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       if (tc::elect_one()) tc::mma_commit(mma_done);  // arrives once every MMA issued above has retired
     } else if (warp == 2) {  // items
       Schedule sched(a);
-      for (int n = 0;; ++n) {
-        // to and fro; the last round, which has items for some CTAs only, for those with the least so far
-        const bool back = (n & 1) || (n > 0 && (int64_t)(n + 1) * gridDim.x >= sched.total);
-        const int64_t c = back ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
-        const Item it = sched.at((int64_t)n * gridDim.x + c);
+      for (int n = 0, round = 0;; ++n) {
+        const Item it = sched.at(sched.slot(round));
+        round += it.row0 >= 0;  // (an item of no tiles that only passes time keeps the slot)
         // an item takes its tiles' time: one wait for every 2^18 of them (about 0.4 s)
         int waits = 1 + (sched.longest >> 18);
         bool ok = false;
