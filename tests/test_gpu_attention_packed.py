@@ -508,3 +508,29 @@ def test_a_long_sequence_among_many_empty_ones_costs_few_scans(zo):
     assert zo.zo_sync(c) == 0
     assert min(times) < 30.0, times
     c.close()
+
+
+@pytest.mark.parametrize("H,Hk,hd", [(1, 1, 64), (2, 1, 128)])
+def test_a_late_bad_token_of_a_very_long_sequence_ends_no_wait(zo, ctx, H, Hk, hd):
+    """Rows of its tile take seconds to compute again from 600000 keys: nothing in the kernel waits
+    for them, and they come out right."""
+    n, H_all = 600001, H + 2 * Hk
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    qkv = torch.randn(n, H_all * hd, generator=g, device="cuda", dtype=torch.bfloat16)
+    q, k, v = split(qkv, H, Hk, hd)
+    v[n - 1] = math.nan
+    out = torch.zeros(n, H * hd, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets([n]), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    assert torch.isnan(out[n - 1]).all() and torch.isfinite(out[: n - 1]).all()
+    for r in (n - 2, n - 3, n - 34, n // 128 * 128 - 1, 300000):
+        for h in range(H):
+            Q = q[r, h * hd: (h + 1) * hd].double()
+            K, V = k[: r + 1, :hd].double(), v[: r + 1, :hd].double()
+            s = K @ Q / math.sqrt(hd)
+            w = torch.softmax(s, 0)
+            ref, A = w @ V, w @ V.abs()
+            # as above, and a sum of r + 1 fp32 terms in chains of n / 32 at most
+            e = 2 * hd * 2.0 ** -23 * (K.abs() @ Q.abs()).max() / math.sqrt(hd) + 2.0 ** -23 * s.abs().max() + n / 32 * 2.0 ** -23
+            tol = 1.02 * (A * (2.0 ** -8 + 2.0 ** -20 + 2 * e) + 2.0 ** -8 * ref.abs())
+            assert torch.all((out[r, h * hd: (h + 1) * hd].double() - ref).abs() <= tol)

@@ -23,8 +23,8 @@
 //     (or padding): their scores are masked, groups of 16 keys behind the sequence are not
 //     multiplied, and value rows behind it in its last group are cleared in shared memory;
 //   - within the diagonal tile a later token's value row is multiplied by probability 0, which is
-//     not 0 for an infinity or NaN: a row whose output is not finite is looked at again (repair_rows),
-//     and its columns that a later value reached are computed from its own keys alone.
+//     not 0 for an infinity or NaN: a row whose output is not finite is looked at again at the CTA's
+//     end (repair_rows), and its columns that a later value reached are computed from its own keys alone.
 #include <cmath>
 
 #include "zo_attn_packed.cuh"
@@ -245,6 +245,23 @@ struct Schedule {
   }
 };
 
+// The rows of one softmax warp's items (its stream's, 32 from 32 qd on of each tile) again, where their
+// outputs are not finite.  For the end of a CTA: a row takes about 4 us for every 32 keys, and inside the
+// pipeline other warps' bounded waits would have to last that long (32 rows behind 65536 keys: 0.24 s).
+template <int HD>
+__device__ __noinline__ void repair_items(const PackedArgs &a, int i, int qd) {
+  Schedule sched(a);
+  for (int round = 0;;) {
+    const Item w = sched.at(sched.slot(round));
+    round += w.row0 >= 0;
+    if (w.len == 0) break;
+    const int first = (i ? w.q[1] : w.q[0]) + 32 * qd, tiles = i ? w.tiles[1] : w.tiles[0];
+    const int head = i ? w.head[1] : w.head[0], rows = min(32, w.len - first);
+    if (tiles != 0 && rows > 0)
+      repair_rows<HD>(a, w.row0, w.len, first, 0xFFFFFFFFu >> (32 - rows), head, head / a.shared, tiles * kM);
+  }
+}
+
 // One row's step over the first 32 NC keys of a tile: its scores from tensor memory at tS, maximum,
 // probabilities back to the first 16 NC columns there, sum.  MASK: keys behind `last` do not count
 // (their scores may be anything).
@@ -366,8 +383,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     return true;
   };
 
-  // registers of a thread from here on: 4 warps x kFew + 8 x kMany = 12 x 168 of the launch
-  constexpr int kFew = 88, kMany = 208;
+  // Registers of a thread from here on: 4 warps x kFew + 8 x kMany = 12 x 168 of the launch.  With 88 and
+  // 208 the softmax of head dim 64 reloads a spilled word in its loop: 44.8 us for the case of 43.2.
+  constexpr int kFew = 72, kMany = 216;
   if (warp < 4) {
     tc::regs_dec<kFew>();
     if (warp == 0) {
@@ -546,7 +564,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const uint32_t tS = tmem + (uint32_t)(kM * i) + lane_off, tO = tmem + 2u * kM + (uint32_t)(HD * i) + lane_off;
     uint32_t done = 0;  // tiles of the stream so far
     int base = 0;       // key tiles of the items before
-    bool ok = true;
+    bool ok = true, suspect = false;  // this lane's outputs so far hold an infinity or NaN
     for (int n = 0; ok; ++n) {
       if (!tc::warp_wait_fast(&item_full[n % kItems], ring_parity(n, kItems), abort_flag)) {
         ok = false;
@@ -629,12 +647,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&o_free[i]);
-      const uint32_t suspects = __ballot_sync(0xFFFFFFFFu, r < w.len && worst != 0);
-      __syncwarp();
-      if (suspects)
-        repair_rows<HD>(a, w.row0, w.len, q0 + 32 * qd, suspects, head, head / a.shared, tiles * kM);
+      suspect |= r < w.len && worst != 0;
     }
     if (!ok && lane == 0) give_up();
+    if (__any_sync(0xFFFFFFFFu, suspect) && ok) repair_items<HD>(a, i, qd);
   }
   tc::tc_fence_before();
   __syncthreads();

@@ -49,13 +49,15 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len,
   for (; rows; rows &= rows - 1) {
     const int r = first + __ffs(rows) - 1;
     uint16_t *orow = a.out + (int64_t)(row0 + r) * a.ldo + h * HD + C * lane;
-    uint32_t open = 0;  // this lane's columns to compute again
+    uint32_t bad = 0, later = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) bad |= finite_bf16(orow[c]) ? 0u : 1u << c;
+    if (!__any_sync(0xFFFFFFFFu, bad)) continue;
+#pragma unroll 4
     for (int j = r + 1; j < min(key_end, len); ++j)
 #pragma unroll
-      for (int c = 0; c < C; ++c) open |= finite_bf16(V[(int64_t)j * a.ldv + c]) ? 0u : 1u << c;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (finite_bf16(orow[c])) open &= ~(1u << c);
+      for (int c = 0; c < C; ++c) later |= finite_bf16(V[(int64_t)j * a.ldv + c]) ? 0u : 1u << c;
+    const uint32_t open = bad & later;  // this lane's columns to compute again
     if (!__any_sync(0xFFFFFFFFu, open)) continue;
     const uint16_t *q = a.q + (int64_t)(row0 + r) * a.ldq + h * HD;
     float m = -INFINITY, l = 0.f, acc[C] = {};
@@ -64,7 +66,7 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len,
       float s = -INFINITY;
       if (j >= 0) {
         s = 0.f;
-#pragma unroll 1
+#pragma unroll 4
         for (int e = 0; e < HD; e += 8) {
           const uint4 x = *reinterpret_cast<const uint4 *>(q + e);
           const uint4 y = *reinterpret_cast<const uint4 *>(K + (int64_t)j * a.ldk + e);
@@ -90,7 +92,7 @@ __device__ __noinline__ void repair_rows(const PackedArgs &a, int row0, int len,
       m = mx;
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[c] *= f;
-#pragma unroll 4
+#pragma unroll 8
       for (int t = 0; t < min(32, j0 + 1); ++t) {
         const float pt = __shfl_sync(0xFFFFFFFFu, p, t);
 #pragma unroll
