@@ -320,6 +320,7 @@ logprobs_kernel(const LogprobArgs a) {
   const int j_first = (int)((int64_t)row.vectors * part / a.splits);
   const int j_end = (int)((int64_t)row.vectors * (part + 1) / a.splits);
   if (tid == 0) sh.n_hot = sh.n_cand = 0;
+  if (THREADS == 32) __syncwarp();  // (the votes of a warp's selection do not order memory, barriers do)
   if (a.splits > 1) tc::cluster_arrive();  // block 0 has to run before its memory is written
   tc::pdl_wait();
   // the given token's logit, wanted at the end
