@@ -699,8 +699,8 @@ zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void *k, const v
  *   top_ids (int32), top_logprobs (fp32)  device [rows][top]; either may be NULL, top = 0: none.
  * A logit of -inf rules its token out (probability 0).  A row without any other logit, or with
  * a NaN or +inf, has no distribution: its outputs are NaN (NaN logits sort before all others).
- * fp32 sums of a few logits each, joined in fp64 in a fixed order: results do not vary from run to
- * run.  1 <= vocab < 2^31 - 16, vocab <= ld < 2^31, 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP,
+ * fp32 sums of parts of a row (of a few logits each; the entropy's second one of up to a sixteenth of
+ * what a thread reads), joined in fp64 in a fixed order: results do not vary from run to run.  1 <= vocab < 2^31 - 16, vocab <= ld < 2^31, 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP,
  * vocab).  Any alignment of the element type.
  * Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
 zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int64_t rows, int64_t vocab,

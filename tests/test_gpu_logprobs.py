@@ -329,3 +329,21 @@ def test_logprobs_refusals(zo, ctx):
     refused(ids=ids.data_ptr() + 1)
     torch.cuda.synchronize()
     assert torch.all(lp == 9.0) and torch.all(ids == -9)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(1, 1 << 28, "bf16"), (1, (1 << 27) + 5, "f32"), (150, 1 << 22, "f32"),
+                                              (900, 1 << 20, "bf16"), (4000, 9001, "bf16")])
+def test_sums_over_very_many_equal_terms(zo, ctx, rows, vocab, dtype):
+    """Every 997th logit is 1, the others 0: nearly every vector of a thread adds the same, and the
+    roundings of a long fp32 sum would add up, to some 1e-4.  Joined in fp64, what is left are the sums of
+    at most 64 batches of vectors (2^-24 each, and in a batch some 10 steps) in s and u, whose errors enter
+    the entropy as they are, two exponentials (2^-22 each) and the output's rounding."""
+    x = torch.zeros(rows, vocab, dtype=TYPES[dtype], device="cuda")
+    x[:, ::997] = 1.0
+    t = torch.full((rows,), 5, dtype=torch.int32, device="cuda")
+    lp, ent, _, _ = call(zo, ctx, x, t, 0)
+    ones = (vocab + 996) // 997
+    z = ones * math.e + (vocab - ones)
+    H = math.log(z) - ones * math.e / z
+    assert torch.all((lp.double() + math.log(z)).abs() <= 10 * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -24 * math.log(z))
+    assert torch.all((ent.double() - H).abs() <= 84 * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -24 * H)
