@@ -707,7 +707,8 @@ zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int64_t rows, 
                       int64_t ld, const int32_t *targets, float *logprob, float *entropy, int32_t top,
                       int32_t *top_ids, float *top_logprobs);
 
-/* Bytes of device workspace that zo_head_logprobs needs for these sizes (host only).
+/* Bytes of device workspace that zo_head_logprobs needs for these sizes; enough for fewer rows or
+ * tokens too (host only).
  * Errors: ZO_ERR_INVALID (null, sizes outside zo_head_logprobs' limits). */
 zo_status zo_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t *bytes);
 

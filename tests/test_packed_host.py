@@ -193,3 +193,13 @@ def test_scans_of_distinct_lengths_find_the_same_items(lens, rows, group):
         got = list(_items_by_distinct_lengths(cu, total, rows, group, grid))
         assert [i for _, i in got] == list(_items(cu, total, rows, group, grid))
         assert all(s <= distinct for s, _ in got)
+
+
+@pytest.mark.parametrize("vocab", [1, 33, 1000, 2400, 50272, 151936])
+def test_head_workspace_serves_smaller_calls(zo, vocab):
+    """A workspace for so many rows (or tokens) is enough for fewer."""
+    need = [zo.zo_head_logprobs_workspace(rows, vocab) for rows in range(1, 1300)]
+    assert need == sorted(need)
+    for rows in (1, 128, 129, 600):
+        need = [zo.zo_head_logprobs_workspace(rows, v) for v in range(max(1, vocab - 300), vocab + 300)]
+        assert need == sorted(need)

@@ -15,6 +15,7 @@
 // range may be narrower (the MMA's N and the number of loaded boxes follow).  More rows run on CTA
 // pairs (cta_group::2): 256 rows, each CTA holding 128 of them and half of W's tile, which takes two
 // thirds of the shared-memory traffic; ranges in units of 64.
+#include <algorithm>
 #include <cmath>
 
 #include "zo_internal.cuh"
@@ -603,8 +604,17 @@ bool head_sizes_ok(int64_t rows, int64_t vocab) {
   return rows >= 1 && rows < INT32_MAX - 256 && vocab >= 1 && vocab < INT32_MAX - 512;
 }
 
-int64_t head_bytes(int64_t rows, int64_t vocab) {
+int64_t head_bytes_of(int64_t rows, int64_t vocab) {
   return rows * (head_shape(rows, vocab).most * (int64_t)sizeof(float4)) + ((rows * 4 + 15) / 16) * 16;
+}
+
+// Enough for these rows and for fewer, some of which take more ranges: those of one CTA, and those of
+// the last row of one, two, .. row tiles, up to where the number of ranges no longer falls.
+int64_t head_bytes(int64_t rows, int64_t vocab) {
+  int64_t most = std::max(head_bytes_of(rows, vocab), head_bytes_of(std::min<int64_t>(rows, kBM), vocab));
+  for (int64_t tiles = 1; tiles * 32 < kSmCount / 2; ++tiles)
+    most = std::max(most, head_bytes_of(std::min<int64_t>(rows, tiles * HeadCfg<true>::kRows), vocab));
+  return most;
 }
 
 }  // namespace
