@@ -243,3 +243,73 @@ def test_head_refusals(zo, ctx):
     refused(lp=lp.data_ptr() + 2)
     torch.cuda.synchronize()
     assert torch.all(lp == 9.0)
+
+
+def exact_scores(x, t):
+    """(logprob, entropy, sum_j p_j (max - x_j)) of exact logits, in 64 bits."""
+    ref = torch.log_softmax(x, 1)
+    p = ref.exp()
+    spread = torch.where(p > 0, p * (x.amax(1, keepdim=True) - x), torch.zeros_like(x)).sum(1)
+    return ref.gather(1, t.long()[:, None])[:, 0], -(p * torch.where(p > 0, ref, torch.zeros_like(ref))).sum(1), spread
+
+
+@pytest.mark.parametrize("rows", [5, 200])
+@pytest.mark.parametrize("width", [2048, 4096, 4104])
+def test_small_products_stand_beside_large_ones_over_wide_widths(zo, ctx, rows, width):
+    """Logits of 1024 from the first column, and 2^-19 from every one behind the first accumulator: one
+    accumulator over the whole width would lose all of those (16 at a time are a quarter of its last bit),
+    accumulators of 1024 or 512 hold them exactly, and so does their sum (whole multiples of 2^-13)."""
+    part, vocab = 1024 if width <= 2048 else 512, 700
+    h, w = torch.zeros(rows, width, device="cuda"), torch.zeros(vocab, width, device="cuda")
+    h[:, 0], h[:, part:] = 32.0, 2.0 ** -9
+    w[:, 0] = 31.75
+    w[::7, 0] = 32.0
+    w[::14, part: width // 64 * 64] = 2.0 ** -10
+    h, w = h.to(torch.bfloat16), w.to(torch.bfloat16)
+    t = (torch.arange(rows, device="cuda") % 50 * 7).to(torch.int32)
+    lp, ent = call(zo, ctx, h, w, t)
+    want, want_h, spread = exact_scores(h.double() @ w.double().T, t)
+    # exponentials (2^-22), chains of 10, arguments up to 14 (2^-24 each): the small products matter 2e-3
+    E = 2.0 ** -22 + 10 * 2.0 ** -24 + 2.0 ** -24 * (1 + spread)
+    assert torch.all((lp.double() - want).abs() <= E + 2.0 ** -24 * want.abs())
+    assert torch.all((ent.double() - want_h).abs() <= E * (3 + 2 * spread) + 2.0 ** -24 * want_h)
+    assert (want[0] - want[1]).abs() > 1e-3  # (tokens 0 and 7: with the small products and without)
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 50272), (300, 50272), (5, 151936)])
+def test_statistics_of_exact_logits(zo, ctx, rows, vocab):
+    """Logits that are one product each, so that only the statistics are off: 32 columns at a time in fp32
+    (exponentials 2^-22, four chains of 8 and their sum, arguments 2^-24 of their size), beyond in fp64."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn(vocab, generator=g, device="cuda") * 3).to(torch.bfloat16)
+    h, w = torch.zeros(rows, 8, device="cuda"), torch.zeros(vocab, 8, device="cuda", dtype=torch.bfloat16)
+    h[:, 0] = torch.tensor([1.0, 0.5, 1.25], device="cuda")[torch.arange(rows, device="cuda") % 3]
+    w[:, 0] = x
+    h = h.to(torch.bfloat16)
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    lp, ent = call(zo, ctx, h, w, t)
+    for r in (0, 1, 2):
+        want, want_h, spread = exact_scores(h[r: r + 1].double() @ w.double().T, t[r: r + 1])
+        E = 2.0 ** -22 + 10 * 2.0 ** -24 + 2.0 ** -24 * (1 + spread)
+        gap = 2.0 ** -25 * 40
+        assert (lp[r].double() - want).abs() <= E + gap + 2.0 ** -24 * want.abs()
+        assert (ent[r].double() - want_h).abs() <= E * (3 + 2 * spread) + 2.0 ** -24 * want_h
+    same = torch.arange(rows, device="cuda") % 3
+    assert torch.equal(ent, ent[:3][same])
+
+
+@pytest.mark.parametrize("rows", [4, 200])
+def test_entropy_where_one_token_has_nearly_all(zo, ctx, rows):
+    """One logit of 20, the others 0: entropies of 2e-3 and less, off by the largest token's exponential
+    (2^-22) and the chains that it stands in (10 steps each of s and u)."""
+    vocab = 50272
+    h, w = torch.zeros(rows, 8, device="cuda"), torch.zeros(vocab, 8, device="cuda")
+    h[:, 0], w[777, 0] = 1.0, 20.0
+    w[778, 1] = 4.0
+    h[:, 1] = (torch.arange(rows, device="cuda") % 5).float()
+    h, w = h.to(torch.bfloat16), w.to(torch.bfloat16)
+    t = torch.full((rows,), 777, dtype=torch.int32, device="cuda")
+    lp, ent = call(zo, ctx, h, w, t)
+    want, want_h, _ = exact_scores(h.double() @ w.double().T, t)
+    assert torch.all((lp.double() - want).abs() <= 2.0 ** -22 + 10 * 2.0 ** -24 + 2.0 ** -19 * want.abs())
+    assert torch.all((ent.double() - want_h).abs() <= 2.0 ** -22 + 20 * 2.0 ** -24 + 2.0 ** -19 * want_h)

@@ -347,3 +347,46 @@ def test_sums_over_very_many_equal_terms(zo, ctx, rows, vocab, dtype):
     H = math.log(z) - ones * math.e / z
     assert torch.all((lp.double() + math.log(z)).abs() <= 10 * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -24 * math.log(z))
     assert torch.all((ent.double() - H).abs() <= 84 * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -24 * H)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(1, 151936), (3, 50272), (300, 50272), (1000, 20000), (4100, 5000)])
+def test_statistics_are_joined_in_64_bits(zo, ctx, dtype, rows, vocab):
+    """Tighter than the bound above, which takes fp32 sums along a thread: a sum is off by its terms
+    (exponential 2^-22, argument two roundings of 2^-24) and the fp32 chains of 4 vectors (s: 8 terms in
+    each of four, and 2 joins) or of a sixteenth of a thread's rounds and those (u), at most 10 + 40."""
+    x, t = logits(rows, vocab, dtype)
+    lp, ent, _, tlp = call(zo, ctx, x, t, 4)
+    for a in range(0, rows, 500):
+        X, T = x[a: a + 500].double(), t[a: a + 500].long()
+        ref = torch.log_softmax(X, 1)
+        p = ref.exp()
+        spread = (p * (X.amax(1, keepdim=True) - X)).sum(1)
+        E = 2.0 ** -22 + 10 * 2.0 ** -24 + 2.0 ** -23 * spread
+        want = ref.gather(1, T[:, None])[:, 0]
+        assert torch.all((lp[a: a + 500].double() - want).abs() <= E + 2.0 ** -24 * want.abs())
+        best = ref.topk(4, 1).values
+        assert torch.all((tlp[a: a + 500].double() - best).abs() <= E[:, None] + 2.0 ** -24 * best.abs())
+        H = -(p * ref).sum(1)
+        assert torch.all((ent[a: a + 500].double() - H).abs() <= E * (1 + 2 * spread) + 40 * 2.0 ** -24 * spread + 2.0 ** -24 * H)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,top", [(1, 151936, 20.0), (2, 50272, 20.0), (300, 50272, 18.0), (1000, 20000, 20.0),
+                                            (4100, 5000, 16.0)])
+def test_entropy_where_one_token_has_nearly_all(zo, ctx, dtype, rows, vocab, top):
+    """One logit stands far above the others, all 0: its exponential is 1 exactly, and of the others only
+    those of its own 4 vectors (32 at most) can vanish beside it in fp32; the rest is relative: 2^-22 of the
+    exponential, two roundings of an argument of 29 at most, chains of 10 and 40."""
+    x = torch.zeros(rows, vocab, device="cuda")
+    at = (torch.arange(rows, device="cuda") * 7919) % vocab
+    x[torch.arange(rows, device="cuda"), at] = top
+    x = x.to(TYPES[dtype])
+    t = at.to(torch.int32)
+    lp, ent, _, _ = call(zo, ctx, x, t, 0)
+    rest = (vocab - 1) * math.exp(-top)
+    H = math.log1p(rest) + rest * top / (1 + rest)
+    lost = 32 * math.exp(-top)
+    rel = 2.0 ** -22 + 2 * 29 * 2.0 ** -24 + 50 * 2.0 ** -24
+    assert torch.all((lp.double() + math.log1p(rest)).abs() <= lost + rel * rest)
+    assert torch.all((ent.double() - H).abs() <= lost + rel * H)
