@@ -203,3 +203,49 @@ def test_head_workspace_serves_smaller_calls(zo, vocab):
     for rows in (1, 128, 129, 600):
         need = [zo.zo_head_logprobs_workspace(rows, v) for v in range(max(1, vocab - 300), vocab + 300)]
         assert need == sorted(need)
+
+
+def _calls(zo, torch):
+    """The operators with tensors of the right types: name of an argument -> a call with it replaced.  The
+    context is closed, so that a call whose types pass is refused by the library without a launch."""
+    ctx = type("Closed", (), dict(handle=None, check=staticmethod(lambda st: (_ for _ in ()).throw(zo.ZoError(st, "")))))()
+    f32, bf, i32 = (lambda n, d=d: torch.zeros(n, dtype=d) for d in (torch.float32, torch.bfloat16, torch.int32))
+
+    def rope(**k):
+        a = dict(dict(x=bf(64), out=bf(64), positions=i32(1)), **k)
+        zo.zo_rope(ctx, a["x"], a["out"], a["positions"], PLAIN, 1, 64, 64, 1, 64)
+
+    def attention(**k):
+        a = dict(dict(q=bf(64), k=bf(64), v=bf(64), out=bf(64), cu_seqlens=i32(2)), **k)
+        zo.zo_attention_packed(ctx, a["q"], a["k"], a["v"], a["out"], a["cu_seqlens"], 1, 1, 64, 64, 64, 64, 1, 1, 64, 1.0)
+
+    def logprobs(**k):
+        a = dict(dict(targets=i32(1), logprob=f32(1), entropy=f32(1), top_ids=i32(2), top_logprobs=f32(2)), **k)
+        zo.zo_logprobs(ctx, f32(8), 1, 8, 8, a["targets"], a["logprob"], a["entropy"], 2, a["top_ids"], a["top_logprobs"])
+
+    def head(**k):
+        a = dict(dict(hidden=bf(8), W=bf(64), targets=i32(1), logprob=f32(1), entropy=f32(1)), **k)
+        zo.zo_head_logprobs(ctx, a["hidden"], a["W"], 1, 8, 8, 8, 8, a["targets"], a["logprob"], a["entropy"], 16, 1 << 20)
+
+    return dict(rope=rope, attention=attention, logprobs=logprobs, head=head)
+
+
+@pytest.mark.parametrize("op,name,wrong", [
+    ("rope", "positions", "int64"), ("rope", "out", "float32"), ("rope", "x", "float16"), ("rope", "out", "float16"),
+    ("attention", "cu_seqlens", "int64"), ("attention", "q", "float16"), ("attention", "k", "float32"),
+    ("attention", "v", "float16"), ("attention", "out", "float32"),
+    ("logprobs", "targets", "int64"), ("logprobs", "logprob", "float64"), ("logprobs", "entropy", "bfloat16"),
+    ("logprobs", "top_ids", "int64"), ("logprobs", "top_logprobs", "float64"),
+    ("head", "hidden", "float16"), ("head", "W", "float32"), ("head", "targets", "int64"),
+    ("head", "logprob", "float64"), ("head", "entropy", "float64")])
+def test_tensors_of_another_type_are_refused(zo, op, name, wrong):
+    """An int64 position would be read as two int32 ones, a double loss written as half of one."""
+    torch = pytest.importorskip("torch")
+    call = _calls(zo, torch)[op]
+    with pytest.raises(zo.ZoError):
+        call()                                   # the right types reach the library
+    if name != "x":
+        with pytest.raises(zo.ZoError):
+            call(**{name: 16})                   # and so does a bare address
+    with pytest.raises(TypeError, match=name if name != "x" else "float16"):
+        call(**{name: torch.zeros(64, dtype=getattr(torch, wrong))})

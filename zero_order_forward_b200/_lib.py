@@ -475,6 +475,8 @@ def zo_layernorm(ctx, x, gamma, beta, out, rows, d):
 
 
 # ------------------------------------------------------------------ packed prompts
+# Tensors are refused (TypeError) where they hold another type than the operator reads or writes: index
+# tensors are int32 here and int64 by torch's default.  Bare addresses are taken as they are.
 
 
 ROPE_SCALINGS = {"none": ZO_ROPE_PLAIN, "linear": ZO_ROPE_LINEAR, "bands": ZO_ROPE_BANDS}
@@ -497,20 +499,41 @@ def _rope_cfg(cfg):
     return cfg if isinstance(cfg, zo_rope_cfg) else zo_rope_cfg.from_dict(cfg)
 
 
-_dtypes = {}
+_F32, _BF16, _I32 = ZO_F32, ZO_BF16, 2
+_TYPE_NAMES = ("float32", "bfloat16", "int32")
+_types = [None] * 3  # torch's, once there is a tensor
 
 
 def _dtype(t, dtype):
     """ZO_F32 / ZO_BF16 of a tensor, unless given."""
     if dtype is not None:
         return int(dtype)
-    if not _dtypes:
+    kind = t.dtype
+    if kind is _types[_BF16]:
+        return ZO_BF16
+    if kind is _types[_F32]:
+        return ZO_F32
+    if _types[0] is None:
         import torch
-        _dtypes.update({torch.float32: ZO_F32, torch.bfloat16: ZO_BF16})
-    code = _dtypes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{t.dtype}: float32 or bfloat16 expected")
-    return code
+        _types[:] = torch.float32, torch.bfloat16, torch.int32
+        return _dtype(t, dtype)
+    raise TypeError(f"{kind}: float32 or bfloat16 expected")
+
+
+def _typed(t, code, name):
+    """Address of a tensor of that type; an address is taken as it is."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is _types[code]:
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
+    if _types[0] is None:
+        import torch
+        _types[:] = torch.float32, torch.bfloat16, torch.int32
+        return _typed(t, code, name)
+    raise TypeError(f"{name}: {t.dtype}, {_TYPE_NAMES[code]} expected")
 
 
 def zo_rope_frequencies(cfg):
@@ -525,23 +548,28 @@ def zo_rope_frequencies(cfg):
 
 
 def zo_rope(ctx, x, out, positions, cfg, rows, ldx, ldo, n_heads, head_dim, dtype=None):
-    """cfg: a zo_rope_cfg, or a dict of its fields (scaling "none", "linear" or "bands")."""
-    return ctx.check(_L.zo_rope(ctx.handle, _ptr(x), _ptr(out), _dtype(x, dtype), _ptr(positions),
-                                ctypes.byref(_rope_cfg(cfg)), rows, ldx, ldo, n_heads, head_dim))
+    """cfg: a zo_rope_cfg, or a dict of its fields (scaling "none", "linear" or "bands").  The types of x
+    and out are taken from x, unless dtype says what they hold."""
+    code = _dtype(x, dtype)
+    return ctx.check(_L.zo_rope(ctx.handle, _ptr(x), _ptr(out) if dtype is not None else _typed(out, code, "out"), code,
+                                _typed(positions, _I32, "positions"), ctypes.byref(_rope_cfg(cfg)), rows, ldx, ldo,
+                                n_heads, head_dim))
 
 
 def zo_attention_packed(ctx, q, k, v, out, cu_seqlens, n_seqs, total_tokens, ldq, ldk, ldv, ldo,
                         n_heads, n_kv_heads, head_dim, scale):
-    return ctx.check(_L.zo_attention_packed(ctx.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                            _ptr(cu_seqlens), n_seqs, total_tokens, ldq, ldk, ldv,
+    return ctx.check(_L.zo_attention_packed(ctx.handle, _typed(q, _BF16, "q"), _typed(k, _BF16, "k"),
+                                            _typed(v, _BF16, "v"), _typed(out, _BF16, "out"),
+                                            _typed(cu_seqlens, _I32, "cu_seqlens"), n_seqs, total_tokens, ldq, ldk, ldv,
                                             ldo, n_heads, n_kv_heads, head_dim, scale))
 
 
 def zo_logprobs(ctx, logits, rows, vocab, ld, targets, logprob, entropy, top=0, top_ids=None,
                 top_logprobs=None, dtype=None):
     return ctx.check(_L.zo_logprobs(ctx.handle, _ptr(logits), _dtype(logits, dtype), rows, vocab, ld,
-                                    _ptr(targets), _ptr(logprob), _ptr(entropy), top, _ptr(top_ids),
-                                    _ptr(top_logprobs)))
+                                    _typed(targets, _I32, "targets"), _typed(logprob, _F32, "logprob"),
+                                    _typed(entropy, _F32, "entropy"), top, _typed(top_ids, _I32, "top_ids"),
+                                    _typed(top_logprobs, _F32, "top_logprobs")))
 
 
 def zo_head_logprobs_workspace(rows, vocab):
@@ -558,8 +586,9 @@ def zo_head_logprobs(ctx, hidden, W, rows, vocab, width, ldh, ldw, targets, logp
     """workspace: a device tensor (its size is taken) or an address with workspace_bytes."""
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    return ctx.check(_L.zo_head_logprobs(ctx.handle, _ptr(hidden), _ptr(W), rows, vocab, width, ldh,
-                                         ldw, _ptr(targets), _ptr(logprob), _ptr(entropy),
+    return ctx.check(_L.zo_head_logprobs(ctx.handle, _typed(hidden, _BF16, "hidden"), _typed(W, _BF16, "W"), rows,
+                                         vocab, width, ldh, ldw, _typed(targets, _I32, "targets"),
+                                         _typed(logprob, _F32, "logprob"), _typed(entropy, _F32, "entropy"),
                                          _ptr(workspace), workspace_bytes))
 
 
