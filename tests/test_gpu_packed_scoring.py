@@ -268,3 +268,41 @@ def test_a_loss_pass_behind_an_operator_reads_what_it_wrote(zo, stream):
         assert zo.zo_sync(ctx) == 0
         assert losses[0] != 0 and losses[0] == losses[1]
     ctx.close()
+
+
+@pytest.mark.parametrize("op", ["rope", "attention short", "attention", "logprobs", "head"])
+def test_a_launch_that_fails_does_not_fail_the_next_call(zo, stream, op):
+    """A stream whose capture has been invalidated (on the host) takes no launch: the call says so, and the
+    one after it, with the capture over, does what it does."""
+    import ctypes
+    cu = ctypes.CDLL("libcuda.so.1")
+    n = 300
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    ctx = zo.zo_create(torch.zeros(64, **bf), stream=stream)
+    x, out, f = torch.randn(n, 64, device="cuda").to(torch.bfloat16), torch.zeros(n, 64, **bf), torch.zeros(n, device="cuda")
+    offsets = torch.tensor([0, n] if op == "attention" else [0, 20, n], dtype=torch.int32, device="cuda")
+    targets, space = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def call():
+        if op == "rope":
+            zo.zo_rope(ctx, x, out, None, dict(theta=1.0e4, rot_dim=64), n, 64, 64, 1, 64)
+        elif op.startswith("attention"):
+            zo.zo_attention_packed(ctx, x, x, x, out, offsets, len(offsets) - 1, n, 64, 64, 64, 64, 1, 1, 64, 0.125)
+        elif op == "logprobs":
+            zo.zo_logprobs(ctx, x, n, 64, 64, targets, f, None)
+        else:
+            zo.zo_head_logprobs(ctx, x, x, n, n, 64, 64, 64, targets, f, None, space)
+
+    call()
+    assert zo.zo_sync(ctx) == 0
+    handle, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+    assert cu.cuStreamBeginCapture_v2(handle, 2) == 0      # CU_STREAM_CAPTURE_MODE_RELAXED
+    assert cu.cuStreamSynchronize(handle) != 0             # not allowed in a capture, which ends it
+    with pytest.raises(zo.ZoError) as e:
+        call()
+    assert e.value.status == zo.ZO_ERR_CUDA
+    assert cu.cuStreamEndCapture(handle, ctypes.byref(graph)) != 0
+    h, w = torch.ones(8, 64, device="cuda"), torch.ones(64, **bf)
+    zo.zo_rmsnorm(ctx, h, w, out, 8, 64, 0.0)
+    assert zo.zo_sync(ctx) == 0 and torch.all(out[:8] == 1.0)
+    ctx.close()

@@ -240,6 +240,12 @@ void ktime_end(zo_ctx *ctx, int slot, int cls, double work);
 zo_status step_device(zo_ctx *ctx, const double *loss_plus, const double *loss_minus, int32_t n_pert,
                       const double *loss0, float lr, float eps, float damping);
 
+// An error that its caller reports, and that no later launch check is to find.
+inline cudaError_t taken(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // Launch that may start before the kernel ahead of it in the stream has ended (its blocks wait
 // for that end themselves: tc::pdl_wait, before they touch anything but their own memory).  A kernel
 // that writes what a caller may hand on does not let its successor start early (only head_kernel does,
@@ -256,14 +262,14 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  return taken(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...));
 }
 
 // Makes a context's device current for a call and puts the caller's back at its end.
 struct DeviceScope {
   explicit DeviceScope(const zo_ctx *ctx) {
-    if (cudaGetDevice(&before) != cudaSuccess) before = -1;
-    if (before != ctx->device) status = cudaSetDevice(ctx->device);
+    if (taken(cudaGetDevice(&before)) != cudaSuccess) before = -1;
+    if (before != ctx->device) status = taken(cudaSetDevice(ctx->device));
   }
   ~DeviceScope() {
     int now = -1;

@@ -577,7 +577,7 @@ cudaError_t launch_one(const LogprobArgs &a, int64_t rows, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a);
+  return taken(cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a));
 }
 
 template <typename T>
