@@ -45,9 +45,10 @@ constexpr uint32_t kBox = kM * 128;    // bytes of one 128-row x 64-column bf16 
 constexpr int kItems = 2;              // items on hand
 
 // Sequences of at most kShortSeq tokens go to a kernel of their own where the mean length (the buffer's
-// over their number; lengths are known on the device only) lets there be many of them.  16 heads of
-// 128: 64 sequences of 16 tokens take 7.8 us instead of 16.4, 64 of 32 9.7 instead of 16.4; 64 of 64, of
-// which it finds none, 20.6 instead of 19.2, and sequences of some thousand tokens as much more.
+// over their number; lengths are known on the device only) lets there be many of them.  16 query and 8
+// key/value heads of 128: 64 sequences of 16 tokens take 8.3 us instead of 16.4, 64 of 32 10.1 instead of
+// 16.5, 2000 of one 84 instead of 341; where it finds none, 64 of 64 take 22.0 instead of 20.0 and 64 of
+// 128 28.5 instead of 25.4.
 constexpr int kShortMean = 256;
 
 // From this many sequences on, up to 32 long ones among them are held in the lanes of the warp that
@@ -107,26 +108,6 @@ __device__ __forceinline__ int tiles_of(const PackedArgs &a, int shift, const Se
   return s.len <= a.handled ? 0 : (int)(((uint32_t)s.len + (1u << shift) - 1u) >> shift);
 }
 
-// What one warp finds in the sequences from the 33rd on.
-struct Scan {
-  int longer, below;  // sequences of more than `level` tiles; the most tiles of the others
-  int tiles;          // of all (each lane its own)
-  bool bad;
-};
-__device__ __forceinline__ Scan scan_rest(const PackedArgs &a, int shift, int level) {
-  const int lane = threadIdx.x & 31;
-  Scan f{0, 0, 0, false};
-#pragma unroll 1
-  for (int i0 = 32; i0 < a.n_seqs; i0 += 32) {
-    const Seq s = load_seq(a, i0 + lane);
-    const int t = tiles_of(a, shift, s);
-    f.longer += t > level ? 1 : 0;
-    f.below = max(f.below, t > level ? 0 : t);
-    f.tiles += t;
-    f.bad |= s.bad;
-  }
-  return f;
-}
 // The number of the lane-th of the `count` (at most 32) sequences of more than `level` tiles.
 __device__ __forceinline__ int hold(const PackedArgs &a, int shift, int level, int count) {
   const int lane = threadIdx.x & 31;
@@ -146,7 +127,7 @@ __device__ __forceinline__ int hold(const PackedArgs &a, int shift, int level, i
 // The offsets are scanned once for every distinct number of tiles that occurs (as many sequences have
 // more than t tiles for all t between two such numbers); where the offsets are many, up to 32 sequences
 // that are that long are held in the lanes.  One sequence of 16384 tokens among 131072 empty ones took
-// 137 ms with a scan for every number of tiles, 3.2 so.
+// 137 ms with a scan for every number of tiles, 2.7 so.
 struct Schedule {
   const PackedArgs &a;
   int shift, group;        // log2 of a tile's rows; items of one tile (heads, or pairs of them)
@@ -166,11 +147,14 @@ struct Schedule {
     first = load_seq(a, lane);
     int tiles = tiles_of(first), most = tiles;  // (fewer than 2^25 in all)
     bool bad = first.bad;
-    if (a.n_seqs > 32) {
-      const Scan f = scan_rest(a, shift, INT32_MAX);
-      most = max(most, f.below);
-      tiles += f.tiles;
-      bad |= f.bad;
+    // (unrolled, four steps' loads are on their way together: 2000 sequences of one token 84.5 us, not 93)
+#pragma unroll 4
+    for (int i0 = 32; i0 < a.n_seqs; i0 += 32) {
+      const Seq s = load_seq(a, i0 + lane);
+      const int t = tiles_of(s);
+      most = max(most, t);
+      tiles += t;
+      bad |= s.bad;
     }
     if (blockIdx.x == 0 && bad) atomicOr(a.err, ZO_FLAG_OFFSETS);
     total = (int64_t)__reduce_add_sync(0xFFFFFFFFu, tiles) * group;
@@ -185,15 +169,16 @@ struct Schedule {
   __device__ __forceinline__ bool few() const { return a.n_seqs > kManySeqs && count <= 32; }
   // One scan for the new `level` (two where the sequences are held).
   __device__ __forceinline__ void count_level() {
-    const int t = tiles_of(first);
-    count = __popc(__ballot_sync(0xFFFFFFFFu, t > level));
-    below = __reduce_max_sync(0xFFFFFFFFu, t > level ? 0 : t);
-    if (a.n_seqs > 32) {
-      const Scan f = scan_rest(a, shift, level);
-      count += __reduce_add_sync(0xFFFFFFFFu, f.longer);
-      below = max(below, __reduce_max_sync(0xFFFFFFFFu, f.below));
-      if (few()) held = hold(a, shift, level, count);
+    int n = 0, low = 0;
+#pragma unroll 1  // (this code is on the way to the first item: unrolled too, 64 sequences of 128 cost 1.7 us more)
+    for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
+      const int t = tiles_of(i0 == 0 ? first : load_seq(a, i0 + lane));
+      n += t > level ? 1 : 0;
+      low = max(low, t > level ? 0 : t);
     }
+    count = __reduce_add_sync(0xFFFFFFFFu, n);
+    below = __reduce_max_sync(0xFFFFFFFFu, low);
+    if (few()) held = hold(a, shift, level, count);
   }
   // Slot of this CTA's round `n`: to and fro; the last round, which has items for some CTAs only, for
   // those with the least so far.

@@ -12,9 +12,10 @@
 // zo_attn_packed.cu, made for long ones, each takes that kernel's whole chain of hand-overs (loads,
 // scores, softmax, products, output: about 3 us), and one chain runs on an SM at a time.  Here an SM
 // holds a dozen blocks, and a chain has two block barriers.  The warp-level products are slow on this
-// part (about 37 clocks each on an SM quarter, an eighteenth of the tensor pipe's rate): taking
-// sequences of up to 128 this way cost 43 us for 64 of 128 tokens (16 heads of 128) where the
-// pipeline takes 26, and 21 us for 64 of 64 where it takes 19, but 12 us for 64 of 16 where it takes 16.
+// part (about 37 clocks each on an SM quarter, an eighteenth of the tensor pipe's rate), and blocks of more
+// warps, for longer sequences, start late: with 16 query and 8 key/value heads of 128, blocks for up to 128
+// tokens took 60 us for 64 sequences of 128 where the pipeline takes 25, 37 us for 64 of 64 where it takes
+// 20, and 21 us for 64 of 16, which blocks for 32 finish in 8.3.
 #include "zo_attn_packed.cuh"
 
 namespace zo {
