@@ -653,10 +653,12 @@ zo_status zo_rope_frequencies(const zo_rope_cfg *cfg, double *radians);
  *              key heads of a fused projection, pass its rows and n_heads + n_kv_heads).
  *              out == x (with ldo == ldx) rotates in place; otherwise the two must not overlap.
  *   positions  device, int32 [rows] (any value), or NULL: row r has position r.
- * Angles are formed and reduced in fp64 (within 2^-25 of a turn up to position 2^28, 2^-23 at the
- * ends of int32); the rotation is fp32 arithmetic with one rounding to `dtype`.  Best when pointers, row strides and head_dim are
- * multiples of 16 bytes.  1 <= rows < 2^31, 1 <= n_heads <= 65535, rot_dim <= head_dim <=
- * ZO_ROPE_MAX_HEAD_DIM.  Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
+ * Angles are formed and reduced in fp64 (for frequencies of at most one radian per position, which
+ * theta >= 1 and factor >= 1 give: within 2^-25 of a turn up to position 2^28, 2^-23 at the ends of
+ * int32; else a position counts for as many times more); the rotation is fp32 arithmetic with one
+ * rounding to `dtype`.  Best when pointers, row strides and head_dim are multiples of 16 bytes.
+ * 1 <= rows < 2^31, 1 <= n_heads <= 65535, rot_dim <= head_dim <= ZO_ROPE_MAX_HEAD_DIM.
+ * Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
 zo_status zo_rope(zo_ctx *ctx, const void *x, void *out, int dtype, const int32_t *positions,
                   const zo_rope_cfg *cfg, int64_t rows, int64_t ldx, int64_t ldo, int32_t n_heads,
                   int32_t head_dim);
@@ -693,16 +695,16 @@ zo_status zo_attention_packed(zo_ctx *ctx, const void *q, const void *k, const v
  *   top_ids[r][0..top-1] the indices of the top largest logits, largest first, equal values in
  *   the order of their index, and top_logprobs[r][.] = x_id - lse.
  *   logits   device, `dtype` (ZO_F32 or ZO_BF16), rows of ld elements, vocab of them used.
- *   targets  device int32 [rows], or NULL with logprob NULL.  -1 scores nothing: logprob 0.
- *            Any other value outside [0, vocab) gives NaN.
+ *   targets  device int32 [rows], or NULL with logprob NULL.  -1 scores nothing: logprob 0,
+ *            whatever the row holds.  Any other value outside [0, vocab) gives NaN.
  *   logprob, entropy  device fp32 [rows], either may be NULL.
  *   top_ids (int32), top_logprobs (fp32)  device [rows][top]; either may be NULL, top = 0: none.
  * A logit of -inf rules its token out (probability 0).  A row without any other logit, or with
  * a NaN or +inf, has no distribution: its outputs are NaN (NaN logits sort before all others).
  * fp32 sums of parts of a row (of a few logits each; the entropy's second one of up to a sixteenth of
- * what a thread reads), joined in fp64 in a fixed order: results do not vary from run to run.  1 <= vocab < 2^31 - 16, vocab <= ld < 2^31, 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP,
- * vocab).  Any alignment of the element type.
- * Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
+ * what a thread reads), joined in fp64 in a fixed order: results do not vary from run to run.
+ * 1 <= vocab < 2^31 - 16, vocab <= ld < 2^31, 1 <= rows < 2^31, 0 <= top <= min(ZO_MAX_TOP, vocab).
+ * Any alignment of the element type.  Errors: ZO_ERR_INVALID, ZO_ERR_CUDA. */
 zo_status zo_logprobs(zo_ctx *ctx, const void *logits, int dtype, int64_t rows, int64_t vocab,
                       int64_t ld, const int32_t *targets, float *logprob, float *entropy, int32_t top,
                       int32_t *top_ids, float *top_logprobs);
@@ -722,8 +724,9 @@ zo_status zo_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t *bytes
  *   workspace  device, 16-byte aligned, zo_head_logprobs_workspace bytes; holds nothing between
  *              calls.  Calls that may run at the same time need one each.
  * Finite logits within +-1e8; -inf, NaN and +inf as in zo_logprobs.  width, ldh and ldw multiples
- * of 8, hidden and W 16-byte aligned, rows, vocab, width, ldh, ldw >= 1 and < 2^31.  Bounded waits as zo_gemm_bf16.  Errors: ZO_ERR_INVALID (also a
- * workspace that is too small), ZO_ERR_CUDA. */
+ * of 8, hidden and W 16-byte aligned; 1 <= rows < 2^31 - 257, 1 <= vocab < 2^31 - 513, 1 <= width <
+ * 2^31 - 65, ldh and ldw >= width and < 2^31.  Bounded waits as zo_gemm_bf16.
+ * Errors: ZO_ERR_INVALID (also a workspace that is too small), ZO_ERR_CUDA. */
 zo_status zo_head_logprobs(zo_ctx *ctx, const void *hidden, const void *W, int64_t rows, int64_t vocab,
                            int64_t width, int64_t ldh, int64_t ldw, const int32_t *targets,
                            float *logprob, float *entropy, void *workspace, int64_t workspace_bytes);

@@ -249,3 +249,10 @@ def test_tensors_of_another_type_are_refused(zo, op, name, wrong):
             call(**{name: 16})                   # and so does a bare address
     with pytest.raises(TypeError, match=name if name != "x" else "float16"):
         call(**{name: torch.zeros(64, dtype=getattr(torch, wrong))})
+
+
+def test_head_limits_are_those_of_the_header(zo):
+    assert zo.zo_head_logprobs_workspace(2 ** 31 - 258, 8) > 0 and zo.zo_head_logprobs_workspace(1, 2 ** 31 - 514) > 0
+    for rows, vocab in ((2 ** 31 - 257, 8), (1, 2 ** 31 - 513)):
+        with pytest.raises(zo.ZoError):
+            zo.zo_head_logprobs_workspace(rows, vocab)
