@@ -534,3 +534,36 @@ def test_a_late_bad_token_of_a_very_long_sequence_ends_no_wait(zo, ctx, H, Hk, h
             e = 2 * hd * 2.0 ** -23 * (K.abs() @ Q.abs()).max() / math.sqrt(hd) + 2.0 ** -23 * s.abs().max() + n / 32 * 2.0 ** -23
             tol = 1.02 * (A * (2.0 ** -8 + 2.0 ** -20 + 2 * e) + 2.0 ** -8 * ref.abs())
             assert torch.all((out[r, h * hd: (h + 1) * hd].double() - ref).abs() <= tol)
+
+
+@pytest.mark.parametrize("H,Hk,hd", [(4, 2, 128), (2, 2, 64), (3, 3, 64)])
+@pytest.mark.parametrize("lens", [[500, 40, 9], [30, 9, 17]])
+def test_infinities_in_many_rows(zo, ctx, H, Hk, hd, lens):
+    """Value columns that are infinite in every row, from a row on, up to a row, or with either sign in turn:
+    every row is looked at again, for several columns and with several rows at a time."""
+    qkv = make(lens, H, Hk, hd)
+    q, k, v = split(qkv, H, Hk, hd)
+    at = torch.arange(sum(lens), device="cuda")
+    v[:, 5] = math.inf
+    v[:, 6] = torch.where(at % 2 == 0, math.inf, -math.inf).to(torch.bfloat16)
+    v[:, hd - 1] = -math.inf
+    v[lens[0] - 7:, 8] = math.inf
+    v[:13, 9] = -math.inf
+    v[20:, 9] = math.nan
+    v[7:, 33] = math.nan
+    out = torch.zeros(sum(lens), H * hd, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets(lens), H, Hk, hd)
+    assert zo.zo_sync(ctx) == 0
+    ref, tol = by_definition(q, k, v, lens, H, Hk, hd, 1 / math.sqrt(hd))
+    ok = same_or_close(out, ref, tol)
+    assert ok.all(), (~ok).nonzero()[:8].tolist()
+
+
+def test_as_many_sequences_as_there_may_be(zo, ctx):
+    """2^24 of them, a few long: the warps that wait for items wait for scans of all."""
+    lens = [1300, 40, 900, 300, 2000, 128, 700]
+    qkv = make(lens, 2, 1, 64)
+    out = torch.zeros(sum(lens), 128, dtype=torch.bfloat16, device="cuda")
+    call(zo, ctx, qkv, out, offsets(scattered(1 << 24, lens)), 2, 1, 64)
+    assert zo.zo_sync(ctx) == 0
+    check(zo, ctx, qkv, out, lens, 2, 1, 64)

@@ -313,3 +313,12 @@ def test_entropy_where_one_token_has_nearly_all(zo, ctx, rows):
     want, want_h, _ = exact_scores(h.double() @ w.double().T, t)
     assert torch.all((lp.double() - want).abs() <= 2.0 ** -22 + 10 * 2.0 ** -24 + 2.0 ** -19 * want.abs())
     assert torch.all((ent.double() - want_h).abs() <= 2.0 ** -22 + 20 * 2.0 ** -24 + 2.0 ** -19 * want_h)
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_tokens_that_are_not_scored_give_0_whatever_the_row_holds(zo, ctx, rows):
+    h, w, t = make(rows, 700, 64)
+    h[1, 5] = math.nan
+    t[:2] = -1
+    lp, ent = call(zo, ctx, h, w, t)
+    assert torch.all(lp[:2] == 0) and torch.isnan(ent[1]) and torch.isfinite(ent[0])

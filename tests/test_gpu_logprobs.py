@@ -390,3 +390,12 @@ def test_entropy_where_one_token_has_nearly_all(zo, ctx, dtype, rows, vocab, top
     rel = 2.0 ** -22 + 2 * 29 * 2.0 ** -24 + 50 * 2.0 ** -24
     assert torch.all((lp.double() + math.log1p(rest)).abs() <= lost + rel * rest)
     assert torch.all((ent.double() - H).abs() <= lost + rel * H)
+
+
+@pytest.mark.parametrize("rows", [5, 300, 4100])
+def test_tokens_that_are_not_scored_give_0_whatever_the_row_holds(zo, ctx, rows):
+    x, t = logits(rows, 700, "f32")
+    x[1, 5], x[2] = math.nan, -math.inf
+    t[:3] = -1
+    lp, ent, _, _ = call(zo, ctx, x, t, 0)
+    assert torch.all(lp[:3] == 0) and torch.isnan(ent[1:3]).all() and torch.isfinite(ent[0])

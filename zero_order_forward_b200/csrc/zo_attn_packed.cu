@@ -231,8 +231,9 @@ struct Schedule {
 };
 
 // The rows of one softmax warp's items (its stream's, 32 from 32 qd on of each tile) again, where their
-// outputs are not finite.  For the end of a CTA: a row takes about 4 us for every 32 keys, and inside the
-// pipeline other warps' bounded waits would have to last that long (32 rows behind 65536 keys: 0.24 s).
+// outputs are not finite.  For the end of a CTA: inside the pipeline other warps' bounded waits would have to
+// last as long (32 rows behind 65536 keys: 97 ms at head dim 64, 150 at 128; eight rows at a time 58 and
+// 109, but with registers that cost the pipeline 2 to 6%).
 template <int HD>
 __device__ __noinline__ void repair_items(const PackedArgs &a, int i, int qd) {
   Schedule sched(a);
@@ -243,7 +244,7 @@ __device__ __noinline__ void repair_items(const PackedArgs &a, int i, int qd) {
     const int first = (i ? w.q[1] : w.q[0]) + 32 * qd, tiles = i ? w.tiles[1] : w.tiles[0];
     const int head = i ? w.head[1] : w.head[0], rows = min(32, w.len - first);
     if (tiles != 0 && rows > 0)
-      repair_rows<HD>(a, w.row0, w.len, first, 0xFFFFFFFFu >> (32 - rows), head, head / a.shared, tiles * kM);
+      repair_rows<HD, 4>(a, w.row0, w.len, first, 0xFFFFFFFFu >> (32 - rows), head, head / a.shared, tiles * kM);
   }
 }
 

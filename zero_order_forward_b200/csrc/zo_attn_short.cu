@@ -195,7 +195,7 @@ attn_short_kernel(const __grid_constant__ PackedArgs a) {
   if (bad[0] | bad[1]) {
     uint32_t rows = 0;
     for (int k = 0; k < 16; ++k) rows |= (bad[k / 8] >> (k % 8 * 4) & 15u ? 1u : 0u) << k;
-    repair_rows<HD>(a, seq.row0, seq.len, 16 * tile, rows, h, kvh, 16 * tile + 16);
+    repair_rows<HD, 1>(a, seq.row0, seq.len, 16 * tile, rows, h, kvh, 16 * tile + 16);
   }
 }
 
