@@ -674,11 +674,11 @@ zo_status zo_rope(zo_ctx *ctx, const void *x, void *out, int dtype, const int32_
  *               may be empty.  Rows of out outside every sequence are not written.
  *   scale       finite and > 0 (1/sqrt(head_dim) for the decoders here).
  * fp32 scores and sums, probabilities rounded to bf16 for the second product, one bf16 rounding
- * of the output.  A score of -inf has weight 0; a row of no other is NaN.  A row depends on its sequence's rows up to itself only, whatever the other
- * rows hold (infinities and NaN too); its last bits may differ between calls of other total_tokens
- * or n_seqs, which choose among kernels, and in a value column where a later token's is infinite or NaN.
- * The offsets are read on the device: a decreasing or
- * out-of-range pair raises ZO_FLAG_OFFSETS (seen by zo_sync) and its sequence is skipped.
+ * of the output.  A score of -inf has weight 0; a row of no other is NaN.  A row depends on its
+ * sequence's rows up to itself only, whatever the other rows hold (infinities and NaN too); its last
+ * bits may differ between calls of other total_tokens or n_seqs, which choose among kernels, and in a
+ * value column where a later token's is infinite or NaN.  The offsets are read on the device: a
+ * decreasing or out-of-range pair raises ZO_FLAG_OFFSETS (seen by zo_sync) and its sequence is skipped.
  * n_heads % n_kv_heads == 0, head_dim 64 or 128, pointers 16-byte aligned, row strides multiples
  * of 8 elements, 1 <= total_tokens < 2^31 - 256, 1 <= n_seqs <= 2^24.  Bounded waits as zo_gemm_bf16.
  * Errors: ZO_ERR_INVALID, ZO_ERR_UNSUPPORTED (head_dim), ZO_ERR_CUDA. */
